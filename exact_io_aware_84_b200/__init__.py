@@ -30,6 +30,12 @@ __all__ = [
     "fa_fwd_fp8_workspace_size",
     "fa_fp8_quantize",
     "fa_fwd_fp8",
+    "fa_kv4_pool_bytes",
+    "fa_kv4_pool",
+    "fa_kv4_write",
+    "fa_kv4_read",
+    "fa_fwd_kv4_workspace_size",
+    "fa_fwd_kv4",
     "fa_merge",
     "fa_grad_accumulate",
     "fa_convert",
@@ -47,6 +53,7 @@ __all__ = [
     "FA_ERR_TIMEOUT",
     "FA_ERR_WORKSPACE",
     "FA_ERR_NO_DEVICE",
+    "FA_ERR_PAGE",
     "EXPORTED_SYMBOLS",
 ]
 
@@ -58,6 +65,7 @@ FA_ERR_CUDA = 4
 FA_ERR_TIMEOUT = 5
 FA_ERR_WORKSPACE = 6
 FA_ERR_NO_DEVICE = 7
+FA_ERR_PAGE = 8
 
 FA_BF16 = 0
 FA_FP16 = 1
@@ -84,6 +92,11 @@ _SIGNATURES = {
     "fa_fp8_quantize": (_c_int, [_vp, _vp, _vp, _vp, _vp, _sz, _c_int, _c_int, _c_int, _c_int, _c_int, _vp]),
     "fa_fwd_fp8": (_c_int, [_vp, _vp, _vp, _vp, _vp, _vp, _vp, _sz, _c_int, _c_int, _c_int, _c_int, _c_float,
                             _c_int, _c_int, _vp]),
+    "fa_kv4_pool_bytes": (_sz, [_c_int] * 4),
+    "fa_kv4_write": (_c_int, [_vp] * 6 + [_c_int] * 8 + [_vp]),
+    "fa_kv4_read": (_c_int, [_vp] * 6 + [_c_int] * 8 + [_vp]),
+    "fa_fwd_kv4_workspace_size": (_sz, [_c_int] * 5),
+    "fa_fwd_kv4": (_c_int, [_vp] * 8 + [_sz] + [_c_int] * 8 + [_c_float, _c_int, _c_int, _vp]),
     "fa_merge": (_c_int, [_vp, _vp, _vp, _vp, _vp, _c_int, ctypes.c_longlong, _c_int, _vp]),
     "fa_grad_accumulate": (_c_int, [_vp, _vp, ctypes.c_longlong, _c_int, _vp]),
     "fa_convert": (_c_int, [_vp, _vp, ctypes.c_longlong, _c_int, _vp]),
@@ -493,6 +506,150 @@ def _dense_cuda(name, t, dtypes, ref=None):
         raise ValueError(f"{name} must be a contiguous CUDA tensor of type {dtypes}")
     if ref is not None and t.device != ref.device:
         raise ValueError(f"{name} must be on the same device as the other arguments")
+
+
+def fa_kv4_pool_bytes(n_pages: int, Hkv: int, page: int, d: int) -> int:
+    return int(load_library().fa_kv4_pool_bytes(int(n_pages), int(Hkv), int(page), int(d)))
+
+
+def fa_kv4_pool(n_pages: int, Hkv: int, page: int, d: int, device="cuda"):
+    """An empty 4-bit key/value cache: uint8 [n_pages, Hkv, page/16, 18 d], blocks
+    of 16 tokens (keys, values and scales; the layout is the library's own)."""
+    torch = _torch()
+    if not fa_kv4_pool_bytes(n_pages, Hkv, page, d):
+        raise ValueError(f"no such cache: {n_pages} pages of {page} tokens, {Hkv} heads of {d}")
+    return torch.empty((n_pages, Hkv, page // 16, 18 * d), dtype=torch.uint8, device=device)
+
+
+def _check_kv4(pool, page_table, start, count, like, B, Hkv, d):
+    """The cache arguments of a call whose rows are ``like`` (None: the pool's
+    own device).  Returns (n_pages, page, max_pages)."""
+    torch = _torch()
+    device = pool.device if like is None else like.device
+    if not pool.is_cuda or pool.dtype != torch.uint8 or pool.dim() != 4 or not pool.is_contiguous():
+        raise ValueError("pool must be a contiguous CUDA uint8 tensor [n_pages, Hkv, page/16, 18 d] (fa_kv4_pool)")
+    n_pages, heads, blocks, width = pool.shape
+    if heads != Hkv or width != 18 * d:
+        raise ValueError(f"pool holds {heads} heads of {width // 18}, the call has {Hkv} of {d}")
+    if page_table.dim() != 2 or page_table.shape[0] != B:
+        raise ValueError(f"page_table must be [B, max_pages] with B = {B}")
+    for name, t in (("page_table", page_table), ("start", start), ("count", count)):
+        if t is None and name == "count":
+            continue
+        if not t.is_cuda or t.dtype != torch.int32 or not t.is_contiguous():
+            raise ValueError(f"{name} must be a contiguous CUDA int32 tensor")
+        if t.device != device:
+            raise ValueError(f"{name} is on {t.device}, the rows on {device}: they must share a device")
+        if name != "page_table" and (t.dim() != 1 or t.shape[0] != B):
+            raise ValueError(f"{name} must be [B] with B = {B}")
+    if pool.device != device:
+        raise ValueError(f"pool is on {pool.device}, the rows on {device}: they must share a device")
+    return n_pages, 16 * blocks, page_table.shape[1]
+
+
+def _kv4_call(where, device, stream, fn, *args):
+    """fn(*args, stream) with ``device`` current; raises on a status other than FA_OK."""
+    torch = _torch()
+    if torch.cuda.current_device() == device.index:
+        st = fn(*args, _stream_handle(stream, device))
+    else:
+        with torch.cuda.device(device):
+            st = fn(*args, _stream_handle(stream, device))
+    if st != FA_OK:
+        raise FAError(st, where)
+
+
+def fa_kv4_write(k, v, pool, page_table, start, count=None, stream=None):
+    """Quantise k, v [B, Hkv, T, d] (bf16 or fp16, contiguous) into the 4-bit
+    cache ``pool`` at positions start[b] .. start[b] + T - 1 (the first
+    count[b] of them) of each sequence; see include/fa.h.
+
+    page_table: int32 [B, max_pages]; start, count: int32 [B].
+    """
+    _check_bhnd("k", k)
+    _check_bhnd("v", v)
+    if v.shape != k.shape or v.dtype != k.dtype or v.device != k.device:
+        raise ValueError("k and v must match in shape, dtype and device")
+    B, Hkv, T, d = k.shape
+    n_pages, page, max_pages = _check_kv4(pool, page_table, start, count, k, B, Hkv, d)
+    _kv4_call("fa_kv4_write", k.device, stream, load_library().fa_kv4_write, k.data_ptr(), v.data_ptr(),
+              pool.data_ptr(), page_table.data_ptr(), start.data_ptr(), None if count is None else count.data_ptr(),
+              B, Hkv, T, d, n_pages, page, max_pages, _dtype_code(k))
+
+
+def fa_kv4_read(pool, page_table, start, count=None, N: Optional[int] = None, k=None, v=None, dtype=None,
+                stream=None):
+    """k, v [B, Hkv, N, d] of positions start[b] .. start[b] + N - 1 from the
+    4-bit cache, rows at and after count[b] zero.  ``k`` and ``v`` may be
+    preallocated, else N and ``dtype`` (the type that was written) say what
+    to allocate."""
+    torch = _torch()
+    if pool.dim() != 4:
+        raise ValueError("pool must be [n_pages, Hkv, page/16, 18 d]")
+    if (k is None) != (v is None):
+        raise ValueError("give both k and v, or neither")
+    if k is None:
+        if N is None or dtype not in (torch.bfloat16, torch.float16):
+            raise ValueError("without k and v, give N and dtype (bfloat16 or float16)")
+        shape = (page_table.shape[0], pool.shape[1], N, pool.shape[3] // 18)
+        k = torch.empty(shape, dtype=dtype, device=pool.device)
+        v = torch.empty(shape, dtype=dtype, device=pool.device)
+    _check_bhnd("k", k)
+    _check_bhnd("v", v)
+    if v.shape != k.shape or v.dtype != k.dtype or v.device != k.device:
+        raise ValueError("k and v must match in shape, dtype and device")
+    B, Hkv, rows, d = k.shape
+    if (N is not None and N != rows) or (dtype is not None and dtype != k.dtype):
+        raise ValueError("k and v do not have the N and dtype that are asked for")
+    n_pages, page, max_pages = _check_kv4(pool, page_table, start, count, k, B, Hkv, d)
+    _kv4_call("fa_kv4_read", k.device, stream, load_library().fa_kv4_read, pool.data_ptr(), page_table.data_ptr(),
+              start.data_ptr(), None if count is None else count.data_ptr(), k.data_ptr(), v.data_ptr(),
+              B, Hkv, rows, d, n_pages, page, max_pages, _dtype_code(k))
+    return k, v
+
+
+def fa_fwd_kv4_workspace_size(B: int, H: int, Hkv: int, T: int, d: int) -> int:
+    return int(load_library().fa_fwd_kv4_workspace_size(int(B), int(H), int(Hkv), int(T), int(d)))
+
+
+def fa_fwd_kv4(q, pool, page_table, start, count=None, o=None, lse=None, workspace=None,
+               scale: Optional[float] = None, causal: bool = False, stream=None, o_fp32: bool = False):
+    """O and LSE of q [B, H, T, d] over the 4-bit cache ``pool``, whose Hkv
+    heads divide H: the T tokens at positions start[b] + t have been written
+    already.  Query t sees the keys up to its own (``causal``), or all of
+    start[b] + count[b].  Rows t >= count[b] are padding: O = 0, LSE = -inf.
+
+    A decoding step: fa_kv4_write(k, v, pool, table, start), then
+    fa_fwd_kv4(q, pool, table, start), then start += 1.
+    """
+    torch = _torch()
+    _check_bhnd("q", q)
+    B, H, T, d = q.shape
+    Hkv = pool.shape[1] if pool.dim() == 4 else 0
+    n_pages, page, max_pages = _check_kv4(pool, page_table, start, count, q, B, Hkv, d)
+    if Hkv < 1 or H % Hkv != 0:
+        raise ValueError(f"q's {H} heads are not a multiple of the pool's {Hkv}")
+    if scale is None:
+        scale = 1.0 / float(d) ** 0.5
+    if o is None:
+        o = torch.empty(q.shape, dtype=torch.float32 if o_fp32 else q.dtype, device=q.device)
+    else:
+        _check_bhnd("o", o, q, allow_f32=True)
+    if lse is None:
+        lse = torch.empty((B, H, T), dtype=torch.float32, device=q.device)
+    else:
+        _check_lse(lse, q)
+    lib = load_library()
+    if workspace is None:
+        need = int(lib.fa_fwd_kv4_workspace_size(B, H, Hkv, T, d))
+        workspace = torch.empty(need, dtype=torch.uint8, device=q.device)
+    else:
+        _check_workspace(workspace, q)
+    _kv4_call("fa_fwd_kv4", q.device, stream, lib.fa_fwd_kv4, q.data_ptr(), pool.data_ptr(), page_table.data_ptr(),
+              start.data_ptr(), None if count is None else count.data_ptr(), o.data_ptr(), lse.data_ptr(),
+              workspace.data_ptr(), workspace.numel() * workspace.element_size(), B, H, Hkv, T, d, n_pages, page,
+              max_pages, float(scale), int(bool(causal)), _dtype_code(q, o))
+    return o, lse
 
 
 def fa_merge(o, lse, o_part, lse_part, out=None, stream=None):

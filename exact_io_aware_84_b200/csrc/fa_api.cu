@@ -12,6 +12,7 @@
 
 #include "fa.h"
 #include "fa_kernels.h"
+#include "fa_kv4.cuh"
 #include "sm100_ptx.cuh"
 
 namespace fa {
@@ -156,6 +157,40 @@ int check_common(int B, int H, int N, int d, float scale, int dtype) {
   return FA_OK;
 }
 
+// Sizes of a 4-bit cache call over rows of `heads` heads; *shift gets log2(page).
+int kv4_check_sizes(int B, int heads, int Hkv, int T, int d, int n_pages, int page, int max_pages, int* shift) {
+  if (B <= 0 || heads <= 0 || Hkv <= 0 || heads % Hkv != 0 || T <= 0 || n_pages <= 0 || max_pages <= 0)
+    return FA_ERR_INVALID_ARG;
+  int s = 4;
+  while (s < 8 && (1 << s) != page) ++s;
+  if ((1 << s) != page) return FA_ERR_INVALID_ARG;
+  if (((long long)max_pages << s) >= (1ll << 31)) return FA_ERR_INVALID_ARG;
+  // B * heads in 64 bits first: the product with T could pass 63 bits
+  const long long bh = (long long)B * heads;
+  if (bh >= (1ll << 31) || bh * T >= (1ll << 31)) return FA_ERR_INVALID_ARG;
+  if (d != 64 && d != 128) return FA_ERR_UNSUPPORTED;
+  *shift = s;
+  return FA_OK;
+}
+
+bool aligned4(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
+
+// The cache arguments of a call, checked (sizes by kv4_check_sizes before).
+int kv4_cache(Kv4Cache* c, const void* pool, const int* page_table, const int* start, const int* count, int Hkv,
+              int n_pages, int shift, int max_pages) {
+  if (!pool || !page_table || !start) return FA_ERR_INVALID_ARG;
+  if (!aligned16(pool) || !aligned4(page_table) || !aligned4(start) || !aligned4(count)) return FA_ERR_MISALIGNED;
+  c->pool = static_cast<uint8_t*>(const_cast<void*>(pool));
+  c->table = page_table;
+  c->start = start;
+  c->count = count;
+  c->n_pages = n_pages;
+  c->page_shift = shift;
+  c->max_pages = max_pages;
+  c->Hkv = Hkv;
+  return FA_OK;
+}
+
 uint64_t wait_limit_ns() { return (uint64_t)g_wait_limit_ms.load() * 1000000ull; }
 
 constexpr float kLog2e = 1.4426950408889634f;
@@ -179,6 +214,7 @@ const char* fa_status_string(int s) {
     case FA_ERR_TIMEOUT: return "FA_ERR_TIMEOUT";
     case FA_ERR_WORKSPACE: return "FA_ERR_WORKSPACE";
     case FA_ERR_NO_DEVICE: return "FA_ERR_NO_DEVICE";
+    case FA_ERR_PAGE: return "FA_ERR_PAGE";
     default: return "FA_ERR_UNKNOWN";
   }
 }
@@ -479,6 +515,86 @@ int fa_convert(void* dst, const float* src, long long n, int dst_dtype, void* st
   int st;
   if ((st = device_info(&di)) != FA_OK) return st;
   cudaError_t e = launch_convert(dst_dtype == FA_BF16, dst, src, n, di.sms, static_cast<cudaStream_t>(stream));
+  return e == cudaSuccess ? FA_OK : FA_ERR_CUDA;
+}
+
+size_t fa_kv4_pool_bytes(int n_pages, int Hkv, int page, int d) {
+  int shift;
+  if (kv4_check_sizes(1, Hkv, Hkv, 1, d, n_pages, page, 1, &shift) != FA_OK) return 0;
+  return (size_t)n_pages * Hkv * (page / kKv4Block) * kv4_block_bytes(d);
+}
+
+// fa_kv4_write and fa_kv4_read: the same arguments, k and v in or out.
+static int kv4_rows(bool write, void* k, void* v, const void* pool, const int* page_table, const int* start,
+                    const int* count, int B, int Hkv, int T, int d, int n_pages, int page, int max_pages, int dtype,
+                    void* stream) {
+  if (!k || !v) return FA_ERR_INVALID_ARG;
+  int shift, st = kv4_check_sizes(B, Hkv, Hkv, T, d, n_pages, page, max_pages, &shift);
+  if (st != FA_OK) return st;
+  if (dtype != FA_BF16 && dtype != FA_FP16) return FA_ERR_UNSUPPORTED;
+  Kv4Cache c;
+  if ((st = kv4_cache(&c, pool, page_table, start, count, Hkv, n_pages, shift, max_pages)) != FA_OK) return st;
+  if (!aligned16(k) || !aligned16(v)) return FA_ERR_MISALIGNED;
+  DeviceInfo di;
+  if ((st = device_info(&di)) != FA_OK) return st;
+  if (!(c.status = status_ptr())) return FA_ERR_CUDA;
+  const cudaStream_t s = static_cast<cudaStream_t>(stream);
+  const cudaError_t e = write ? launch_kv4_write(dtype == FA_BF16, d, c, k, v, B, T, s)
+                              : launch_kv4_read(dtype == FA_BF16, d, c, k, v, B, T, s);
+  return e == cudaSuccess ? FA_OK : FA_ERR_CUDA;
+}
+
+int fa_kv4_write(const void* k, const void* v, void* pool, const int* page_table, const int* start,
+                 const int* count, int B, int Hkv, int T, int d, int n_pages, int page, int max_pages, int dtype,
+                 void* stream) {
+  NvtxRange nvtx_range("fa_kv4_write");
+  return kv4_rows(true, const_cast<void*>(k), const_cast<void*>(v), pool, page_table, start, count, B, Hkv, T, d,
+                  n_pages, page, max_pages, dtype, stream);
+}
+
+int fa_kv4_read(const void* pool, const int* page_table, const int* start, const int* count, void* k, void* v, int B,
+                int Hkv, int N, int d, int n_pages, int page, int max_pages, int dtype, void* stream) {
+  NvtxRange nvtx_range("fa_kv4_read");
+  return kv4_rows(false, k, v, pool, page_table, start, count, B, Hkv, N, d, n_pages, page, max_pages, dtype, stream);
+}
+
+size_t fa_fwd_kv4_workspace_size(int B, int H, int Hkv, int T, int d) {
+  int shift;
+  if (kv4_check_sizes(B, H, Hkv, T, d, 1, 16, 1, &shift) != FA_OK) return 0;
+  return 256;
+}
+
+int fa_fwd_kv4(const void* q, const void* pool, const int* page_table, const int* start, const int* count, void* o,
+               float* lse, void* workspace, size_t workspace_bytes, int B, int H, int Hkv, int T, int d, int n_pages,
+               int page, int max_pages, float scale, int causal, int dtype, void* stream) {
+  NvtxRange nvtx_range("fa_fwd_kv4");
+  if (!q || !o || !lse) return FA_ERR_INVALID_ARG;
+  int shift, st = kv4_check_sizes(B, H, Hkv, T, d, n_pages, page, max_pages, &shift);
+  if (st != FA_OK) return st;
+  if (!(scale > 0.f) || scale > 3.0e38f) return FA_ERR_INVALID_ARG;
+  if (dtype != FA_BF16 && dtype != FA_FP16 && dtype != FA_BF16_O_F32 && dtype != FA_FP16_O_F32)
+    return FA_ERR_UNSUPPORTED;
+  Kv4FwdParams p{};
+  if ((st = kv4_cache(&p.c, pool, page_table, start, count, Hkv, n_pages, shift, max_pages)) != FA_OK) return st;
+  if (!aligned16(q) || !aligned16(o) || !aligned16(lse)) return FA_ERR_MISALIGNED;
+  if (!workspace || workspace_bytes < fa_fwd_kv4_workspace_size(B, H, Hkv, T, d)) return FA_ERR_WORKSPACE;
+  if ((reinterpret_cast<uintptr_t>(workspace) & 255u) != 0) return FA_ERR_MISALIGNED;
+  DeviceInfo di;
+  if ((st = device_info(&di)) != FA_OK) return st;
+  if (!(p.c.status = status_ptr())) return FA_ERR_CUDA;
+  p.q = q;
+  p.o = o;
+  p.lse = lse;
+  p.B = B;
+  p.H = H;
+  p.T = T;
+  p.scale_log2 = scale * kLog2e;
+  p.causal = causal != 0;
+  p.wait_limit_ns = wait_limit_ns();
+  p.debug_flags = g_debug_flags.load();
+  const cudaError_t e = launch_kv4_fwd(dtype == FA_BF16 || dtype == FA_BF16_O_F32,
+                                       dtype == FA_BF16_O_F32 || dtype == FA_FP16_O_F32, d, p,
+                                       static_cast<cudaStream_t>(stream));
   return e == cudaSuccess ? FA_OK : FA_ERR_CUDA;
 }
 

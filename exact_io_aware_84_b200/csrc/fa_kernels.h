@@ -131,6 +131,36 @@ cudaError_t launch_merge(int d, int out_kind, float* o, float* lse, const float*
 cudaError_t launch_accumulate(bool bf16, float* acc, const void* src, long long n, int sms, cudaStream_t st);
 cudaError_t launch_convert(bool bf16, void* dst, const float* src, long long n, int sms, cudaStream_t st);
 
+// 4-bit key/value cache (layout in fa_kv4.cuh): what its calls share.
+struct Kv4Cache {
+  uint8_t* pool;       // [n_pages][Hkv][page/16] blocks
+  const int* table;    // [B][max_pages]
+  const int* start;    // [B]: position of the call's first token
+  const int* count;    // [B] tokens of each sequence, or null (= T)
+  int n_pages;
+  int page_shift;      // page = 1 << page_shift tokens
+  int max_pages;
+  int Hkv;
+  int* status;         // device status word
+};
+
+struct Kv4FwdParams {
+  Kv4Cache c;
+  const void* q;       // [B, H, T, D] 16-bit
+  void* o;             // [B, H, T, D] 16-bit, or fp32
+  float* lse;          // [B, H, T]
+  int B, H, T;
+  float scale_log2;    // scale * log2(e)
+  int causal;
+  uint64_t wait_limit_ns;
+  int debug_flags;
+};
+
+cudaError_t launch_kv4_write(bool bf16, int d, const Kv4Cache& c, const void* k, const void* v, int B, int T,
+                             cudaStream_t st);
+cudaError_t launch_kv4_read(bool bf16, int d, const Kv4Cache& c, void* k, void* v, int B, int N, cudaStream_t st);
+cudaError_t launch_kv4_fwd(bool bf16, bool o32, int d, const Kv4FwdParams& p, cudaStream_t st);
+
 int fwd_threads();
 int bwd_threads();
 

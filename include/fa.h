@@ -58,7 +58,8 @@ typedef enum {
   FA_ERR_CUDA = 4,        /* a CUDA runtime / driver call failed */
   FA_ERR_TIMEOUT = 5,     /* a kernel gave up on a pipeline wait */
   FA_ERR_WORKSPACE = 6,   /* workspace missing or smaller than required */
-  FA_ERR_NO_DEVICE = 7    /* no sm_100 device is current */
+  FA_ERR_NO_DEVICE = 7,   /* no sm_100 device is current */
+  FA_ERR_PAGE = 8         /* a kernel met a cache position without a page */
 } fa_status;
 
 /*
@@ -272,14 +273,84 @@ int fa_fwd_fp8(const void* q, const void* k, const void* v, void* o, float* lse,
                void* workspace, size_t workspace_bytes, int B, int H, int N, int d, float scale, int causal,
                int dtype, void* stream);
 
+/*
+ * Serving from a key/value cache held in 4 bits.  New tokens' keys and values
+ * are quantised as they are written into a paged cache; attention reads the
+ * codes as they stand; a stretch of the cache can be read back in 16 bits.
+ * Heads are grouped as in fa_fwd_gqa.  The pages have no counterpart.
+ *
+ * What the cache holds.  Of every 32 elements of a row, ext is the largest if
+ * it exceeds the negative of the smallest, else the smallest.  The scale is
+ * s = -ext/8 rounded to the row's 16-bit type, or 0 if that is below 2^-126 in
+ * magnitude.  Element x is held as n = min(max(floor(x/s + 1/2), -8), 7), or 0
+ * where s = 0, and stands for n s.  NaN is taken as 0 and an infinity as the
+ * largest finite value of its sign, so that what is written is finite.
+ *
+ *   pool       : device buffer of fa_kv4_pool_bytes bytes, 16-byte aligned.  The
+ *                caller allocates it; its content before the first write does
+ *                not matter.  4.5 bits an element; the layout is the library's
+ *                own.  It does not record the 16-bit type: use one dtype for
+ *                all calls on a pool.
+ *   n_pages    : pages in the pool;  page: tokens of a page, 16, 32, 64, 128 or
+ *                256.  A page holds keys and values of all Hkv heads.
+ *   page_table : device int32 [B][max_pages]; position x of sequence b lies in
+ *                page page_table[b][x / page].  Entries of pages that a call
+ *                does not touch are not read as pages and may be anything.
+ *   start      : device int32 [B]; token t of the call is at position
+ *                start[b] + t of its sequence.
+ *   count      : device int32 [B], or NULL for T everywhere: how many of the
+ *                call's T tokens sequence b has (clamped to [0, T]); the rest
+ *                of its rows are padding.
+ * A position below 0 or not below max_pages * page, and a page outside
+ * [0, n_pages), does not exist: it is not written, reads as zeros, is left out
+ * as a key, and fa_last_device_status() reports FA_ERR_PAGE.
+ *
+ * fa_kv4_pool_bytes: bytes of a pool, or 0 for invalid sizes.
+ *
+ * fa_kv4_write: k, v [B, Hkv, T, d], dtype (FA_BF16 or FA_FP16), are quantised
+ *   into the cache.  Bytes of other tokens are left as they are.  Two tokens at
+ *   the same position of the same page leave it undefined.
+ *
+ * fa_kv4_read: k, v [B, Hkv, N, d] <- n s of positions start[b] + i, rounded to
+ *   dtype; rows i >= count[b] are set to zero (count here is out of N).
+ *
+ * fa_fwd_kv4: O and LSE of q [B, H, T, d] over the cache, T tokens of each
+ *   sequence that have been written already.  Query t sees the keys
+ *   0 .. start[b] + t when `causal` is set, else 0 .. start[b] + count[b] - 1.
+ *   Padding rows and rows that see no key get O = 0, LSE = -inf.  n s enters
+ *   unrounded; P s is rounded to fp16 before the product with V's codes, sums
+ *   are float32.  o, lse, scale as in fa_fwd ([B,H,T,d], [B,H,T]; the *_O_F32
+ *   codes store O in float32, as fa_merge takes it).
+ *   workspace: device buffer of fa_fwd_kv4_workspace_size bytes, 256-byte
+ *   aligned, contents ignored on entry; calls that may overlap on the GPU need
+ *   one each.
+ *
+ * Errors: FA_ERR_INVALID_ARG (NULL pointer other than count, non-positive
+ * size, page size, H % Hkv, scale, max_pages * page or row count of 2^31 or
+ * more), FA_ERR_UNSUPPORTED (d, dtype), FA_ERR_MISALIGNED (k, v, q, o, lse,
+ * pool: 16 bytes; page_table, start, count: 4; workspace: 256),
+ * FA_ERR_WORKSPACE, FA_ERR_CUDA, FA_ERR_NO_DEVICE.
+ */
+size_t fa_kv4_pool_bytes(int n_pages, int Hkv, int page, int d);
+int fa_kv4_write(const void* k, const void* v, void* pool, const int* page_table, const int* start,
+                 const int* count, int B, int Hkv, int T, int d, int n_pages, int page, int max_pages, int dtype,
+                 void* stream);
+int fa_kv4_read(const void* pool, const int* page_table, const int* start, const int* count, void* k, void* v, int B,
+                int Hkv, int N, int d, int n_pages, int page, int max_pages, int dtype, void* stream);
+size_t fa_fwd_kv4_workspace_size(int B, int H, int Hkv, int T, int d);
+int fa_fwd_kv4(const void* q, const void* pool, const int* page_table, const int* start, const int* count, void* o,
+               float* lse, void* workspace, size_t workspace_bytes, int B, int H, int Hkv, int T, int d, int n_pages,
+               int page, int max_pages, float scale, int causal, int dtype, void* stream);
+
 /* Human-readable name of a status code (static string, never NULL). */
 const char* fa_status_string(int status);
 
 /*
  * Synchronises `stream`, then returns FA_ERR_TIMEOUT if any kernel of this
  * library on the current device gave up on a pipeline wait since the last
- * call (FA_OK otherwise), and clears that record.  Returns FA_ERR_CUDA if
- * the synchronisation itself fails.
+ * call, FA_ERR_PAGE if one met a cache position without a page (the first of
+ * the two to happen; FA_OK if neither), and clears that record.  Returns
+ * FA_ERR_CUDA if the synchronisation itself fails.
  */
 int fa_last_device_status(void* stream);
 

@@ -31,3 +31,9 @@ from .fp8 import (  # noqa: F401
     fp8_inputs_ref,
     fp8_attn_fwd_ref,
 )
+from .kv4 import (  # noqa: F401
+    round16_ref,
+    kv4_quantise_ref,
+    kv4_values_ref,
+    kv4_attn_ref,
+)
