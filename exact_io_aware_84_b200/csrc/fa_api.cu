@@ -561,7 +561,7 @@ int fa_kv4_read(const void* pool, const int* page_table, const int* start, const
 size_t fa_fwd_kv4_workspace_size(int B, int H, int Hkv, int T, int d) {
   int shift;
   if (kv4_check_sizes(B, H, Hkv, T, d, 1, 16, 1, &shift) != FA_OK) return 0;
-  return 256;
+  return kv4_fwd_workspace(d, (long long)(H / Hkv) * T);
 }
 
 int fa_fwd_kv4(const void* q, const void* pool, const int* page_table, const int* start, const int* count, void* o,
@@ -590,10 +590,9 @@ int fa_fwd_kv4(const void* q, const void* pool, const int* page_table, const int
   p.T = T;
   p.scale_log2 = scale * kLog2e;
   p.causal = causal != 0;
+  p.o32 = dtype == FA_BF16_O_F32 || dtype == FA_FP16_O_F32;
   p.wait_limit_ns = wait_limit_ns();
-  p.debug_flags = g_debug_flags.load();
-  const cudaError_t e = launch_kv4_fwd(dtype == FA_BF16 || dtype == FA_BF16_O_F32,
-                                       dtype == FA_BF16_O_F32 || dtype == FA_FP16_O_F32, d, p,
+  const cudaError_t e = launch_kv4_fwd(dtype == FA_BF16 || dtype == FA_BF16_O_F32, d, p, workspace, di.sms,
                                        static_cast<cudaStream_t>(stream));
   return e == cudaSuccess ? FA_OK : FA_ERR_CUDA;
 }

@@ -144,22 +144,31 @@ struct Kv4Cache {
   int* status;         // device status word
 };
 
+struct Kv4Join;
+
 struct Kv4FwdParams {
   Kv4Cache c;
   const void* q;       // [B, H, T, D] 16-bit
-  void* o;             // [B, H, T, D] 16-bit, or fp32
+  void* o;             // [B, H, T, D] 16-bit, or fp32 when o32
   float* lse;          // [B, H, T]
   int B, H, T;
   float scale_log2;    // scale * log2(e)
   int causal;
+  int o32;
   uint64_t wait_limit_ns;
-  int debug_flags;
+  // set by the launch
+  int row_tiles;             // tiles of query rows a key head
+  long long units_per_seq;   // Hkv * row_tiles
+  Kv4Join* joins;            // [workers]
+  float* partials;           // [workers][2] pieces of results
 };
 
 cudaError_t launch_kv4_write(bool bf16, int d, const Kv4Cache& c, const void* k, const void* v, int B, int T,
                              cudaStream_t st);
 cudaError_t launch_kv4_read(bool bf16, int d, const Kv4Cache& c, void* k, void* v, int B, int N, cudaStream_t st);
-cudaError_t launch_kv4_fwd(bool bf16, bool o32, int d, const Kv4FwdParams& p, cudaStream_t st);
+// Bytes of the attention's workspace; rows = query rows that share a key head.
+size_t kv4_fwd_workspace(int d, long long rows);
+cudaError_t launch_kv4_fwd(bool bf16, int d, const Kv4FwdParams& p, void* workspace, int sms, cudaStream_t st);
 
 int fwd_threads();
 int bwd_threads();

@@ -158,19 +158,18 @@ __global__ void __launch_bounds__(kThreads) fa_kv4_write_kernel(const WriteParam
   uint16_t sk, sv;
   const uint32_t wk = quantise8<BF16>(xk, &sk);
   const uint32_t wv = quantise8<BF16>(xv, &sv);
-  // the even token's lane completes word w of V, the odd one's word w + 1
+  // the even token's lane completes the word of its first four elements of V, the odd one's that of the others
   const uint32_t other = __shfl_xor_sync(0xffffffffu, par ? wv & 0xffffu : wv >> 16, L);
   const bool both = __shfl_xor_sync(0xffffffffu, (int)(blk != nullptr), L) != 0 && blk != nullptr;
   if (blk == nullptr) return;
   const int key = (int)pos & 15, half = key >> 3;
   reinterpret_cast<uint32_t*>(blk)[((half * 8 + (key & 7)) * 4 + l % 4) * W + l / 4] = wk;
-  const int r = 8 * l / (D / 8), w = 8 * l % (D / 8) / 4;
-  uint32_t* vw = reinterpret_cast<uint32_t*>(blk + 8 * D) + ((half * 8 + r) * 4 + ((key & 7) >> 1)) * W + w;
+  uint32_t* vw = reinterpret_cast<uint32_t*>(blk + 8 * D) + ((half * 8 + l % 4 * 2) * 4 + ((key & 7) >> 1)) * W + l / 4;
   if (both) {
-    vw[par] = par ? __byte_perm(other, wv, 0x7610) : __byte_perm(wv, other, 0x5410);
+    vw[4 * W * par] = par ? __byte_perm(other, wv, 0x7610) : __byte_perm(wv, other, 0x5410);
   } else {
     reinterpret_cast<uint16_t*>(vw)[par] = (uint16_t)wv;
-    reinterpret_cast<uint16_t*>(vw + 1)[par] = (uint16_t)(wv >> 16);
+    reinterpret_cast<uint16_t*>(vw + 4 * W)[par] = (uint16_t)(wv >> 16);
   }
   if (l % 4 == 0) {
     uint16_t* s = reinterpret_cast<uint16_t*>(blk + 16 * D) + key * 2 * W + l / 4;
@@ -227,9 +226,9 @@ __global__ void __launch_bounds__(kThreads) fa_kv4_read_kernel(const ReadParams 
       const int key = (int)pos & 15, half = key >> 3;
       const uint16_t* s = reinterpret_cast<const uint16_t*>(blk + 16 * D) + key * 2 * W + l / 4;
       const uint32_t wk = reinterpret_cast<const uint32_t*>(blk)[((half * 8 + (key & 7)) * 4 + l % 4) * W + l / 4];
-      const int r = 8 * l / (D / 8), w = 8 * l % (D / 8) / 4;
-      const uint2 v = *reinterpret_cast<const uint2*>(reinterpret_cast<const uint32_t*>(blk + 8 * D) +
-                                                      ((half * 8 + r) * 4 + ((key & 7) >> 1)) * W + w);
+      const uint32_t* vw =
+          reinterpret_cast<const uint32_t*>(blk + 8 * D) + ((half * 8 + l % 4 * 2) * 4 + ((key & 7) >> 1)) * W + l / 4;
+      const uint2 v = make_uint2(vw[0], vw[4 * W]);
       xk = values8<BF16>(wk, kv4_scale<BF16>(s[0]));
       xv = values8<BF16>(__byte_perm(v.x, v.y, key & 1 ? 0x7632 : 0x5410), kv4_scale<BF16>(s[W]));
     }

@@ -8,8 +8,8 @@
 //               half*8 + g holds the elements 32e + 8t + 0..7 (W = D/32 words
 //               of one lane lie together): low half-word elements 0..3, high
 //               half-word 4..7.
-//   [8D,  16D)  V codes.  Word ((half*8 + r)*4 + t)*W + w holds the elements
-//               r*D/8 + 4w + 0..3 of the keys half*8 + 2t (low half-word) and
+//   [8D,  16D)  V codes.  Word ((half*8 + r)*4 + t)*W + e holds the elements
+//               32e + 4r + 0..3 of the keys half*8 + 2t (low half-word) and
 //               half*8 + 2t + 1 (high half-word).
 //   [16D, 18D)  scales, 16-bit, key by key: W of K, then W of V, one per 32
 //               elements.

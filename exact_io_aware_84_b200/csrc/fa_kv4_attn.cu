@@ -4,8 +4,31 @@
 // P = softmax over the keys j that the row may see, O = sum_j P_j s_V n_V.
 // The codes are used as they stand, never rounded to 16 bits.
 //
-// One CTA per query row, its warps taking the keys in turn with a running
-// maximum and sum each, joined at the end.
+// Work.  A unit is one key head's tile of NT * 8 query rows; its keys are cut
+// into steps of 32.  The steps of all units, laid end to end, are divided
+// evenly over the grid's warps (lengths are known on the device only, so each
+// CTA sums them up first).  A warp that holds a unit from its first to its
+// last step writes the result; the pieces of a unit that lies across warps go
+// to the workspace, and a second kernel joins them.  Sums are in a fixed
+// order: the same call gives the same bits.
+//
+// A step.  The two blocks of 16 keys come by asynchronous bulk copy into a
+// ring that belongs to the warp, ST steps deep, so no warp waits for another.
+//   S^T = K Q^T by mma.m16n8k16, keys as rows and 8 query rows as columns:
+//     nothing is wasted when four or eight query heads share a key head.  A
+//     code's nibble enters an fp16 mantissa (256 + c and 16 + c); the offsets
+//     are taken back by starting each group's sum at -264 or -24 times q's.
+//     The sum over a group of 32 is scaled in float32.  q goes in as fp16: a
+//     bf16 q is brought to 2^14 .. 2^15 per row and group by a power of two,
+//     which the scale takes back (elements 2^31 below the group's largest
+//     round, relative to it, at 2^-40).
+//   O^T = V^T P^T: the head's elements as rows.  V's codes become n by one
+//     fp16 subtraction (exact: a sum over many keys must not carry an offset);
+//     P s_V is rounded to fp16, with s_V taken relative to the largest one so
+//     far (a power of two, which O's end takes back).  P s_V changes from
+//     accumulator to operand order by movmatrix.
+// The running maximum moves only when a score passes it by 2^8: P stays below
+// 2^8 and P s_V below 2^15.
 #include <cuda_runtime.h>
 
 #include "fa.h"
@@ -14,89 +37,618 @@
 #include "sm100_ptx.cuh"
 
 namespace fa {
+
+// What the joining kernel needs to know of the unit that begins in a worker's
+// range and ends behind it (parts = 0: there is none).
+struct Kv4Join {
+  long long row;   // first row of the unit in O and LSE
+  int rows;
+  int parts;       // pieces in the workers that follow
+};
+
 namespace {
 
-constexpr int kThreads = 128;
+constexpr int kWarps = 4;               // of a CTA
+constexpr int kThreads = 32 * kWarps;
+constexpr int kStep = 32;               // keys of a step: two blocks
+constexpr int kBatch = 16;              // steps whose pages a warp looks up at once
+constexpr int kMinSteps = 2;            // least steps worth a warp
+constexpr float kLazy = 8.f;            // log2 by which a score may pass the running maximum
 
-template <bool BF16, int D, bool O32>
-__global__ void __launch_bounds__(kThreads) fa_kv4_fwd_kernel(const Kv4FwdParams p) {
-  constexpr int W = D / 32, NW = kThreads / 32;
+template <int D, int NT>
+struct Shape {
+  static constexpr int W = D / 32, Rows = 8 * NT, Block = kv4_block_bytes(D), Stages = 4;
+  // registers a thread allow this many CTAs a SM
+  static constexpr int CtasPerSm = W * NT <= 4 ? 3 : 2;
+  static constexpr int Slot = Rows * (D + 2);   // floats of a partial result: O, then m and l by row
+  static constexpr size_t Smem = (size_t)kWarps * Stages * 2 * Block;
+};
+
+__device__ __forceinline__ void mma16816(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1,
+                                         const float (&c)[4]) {
+  asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%10,%11,%12,%13};"
+      : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1), "f"(c[0]), "f"(c[1]), "f"(c[2]), "f"(c[3]));
+}
+
+__device__ __forceinline__ uint32_t transpose8x8(uint32_t x) {
+  uint32_t r;
+  asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(x));
+  return r;
+}
+
+__device__ __forceinline__ uint32_t hsub2(uint32_t a, uint32_t b) {
+  __half2 r = __hsub2(*reinterpret_cast<__half2*>(&a), *reinterpret_cast<__half2*>(&b));
+  return *reinterpret_cast<uint32_t*>(&r);
+}
+
+__device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_t bytes, uint32_t bar) {
+  asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(dst),
+               "l"(src), "r"(bytes), "r"(bar)
+               : "memory");
+}
+
+__device__ __forceinline__ float quad_max(float x) {
+  x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 4));
+  x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 8));
+  return fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 16));
+}
+
+__device__ __forceinline__ float quad_sum(float x) {
+  x += __shfl_xor_sync(0xffffffffu, x, 4);
+  x += __shfl_xor_sync(0xffffffffu, x, 8);
+  return x + __shfl_xor_sync(0xffffffffu, x, 16);
+}
+
+__device__ __forceinline__ float pow2(int e) { return __int_as_float((e + 127) << 23); }   // -126 <= e <= 127
+
+// How far sequence b reaches in this call.
+struct Reach {
+  int n, keys, steps;   // tokens, keys that the last of them sees, steps of a unit (at least one)
+  long long start;
+};
+
+__device__ __forceinline__ Reach reach(const Kv4FwdParams& p, int b) {
+  Reach r;
+  r.n = kv4_count(p.c, b, p.T);
+  r.start = p.c.start[b];
+  const long long end = r.n > 0 ? r.start + r.n : 0, cap = (long long)p.c.max_pages << p.c.page_shift;
+  r.keys = (int)(end < 0 ? 0 : end > cap ? cap : end);
+  r.steps = r.keys > 0 ? (int)(((long long)r.keys + kStep - 1) / kStep) : 1;
+  return r;
+}
+
+// A position in the sequence of all steps.
+struct Cursor {
+  int b;
+  long long rem;   // steps behind the first of sequence b
+  Reach r;
+
+  __device__ __forceinline__ void settle(const Kv4FwdParams& p) {
+    while (b < p.B && rem >= (long long)r.steps * p.units_per_seq) {
+      rem -= (long long)r.steps * p.units_per_seq;
+      if (++b < p.B) r = reach(p, b);
+    }
+  }
+};
+
+__device__ __forceinline__ float* slot_of(const Kv4FwdParams& p, long long worker, int which, int slot_floats) {
+  return p.partials + (size_t)(2 * worker + which) * slot_floats;
+}
+
+template <bool BF16, int D, int NT>
+__global__ void __launch_bounds__(kThreads, (Shape<D, NT>::CtasPerSm)) fa_kv4_fwd_kernel(const Kv4FwdParams p) {
+  using Sh = Shape<D, NT>;
+  constexpr int W = Sh::W, ST = Sh::Stages, Block = Sh::Block;
+  extern __shared__ __align__(128) uint8_t ring_all[];
+  __shared__ __align__(8) uint64_t bars[kWarps][ST];
+  __shared__ long long chunk_sum[kThreads + 1], warp_sum[kWarps];
+  __shared__ int abort_flag;
+
+  const int lane = threadIdx.x % 32, warp = threadIdx.x / 32, g = lane / 4, t = lane % 4;
+  uint8_t* const ring = ring_all + (size_t)warp * ST * 2 * Block;
+  const uint32_t bar0 = smem_u32(&bars[warp][0]), ring0 = smem_u32(ring);
+  if (threadIdx.x == 0) abort_flag = 0;
+  if (lane < ST) mbar_init(bar0 + 8 * lane, 2);
+  fence_mbar_init();
   grid_dependency_wait();
   grid_dependents_launch();
-  const int lane = threadIdx.x % 32, warp = threadIdx.x / 32;
-  const long long row = blockIdx.x;
-  const int t = (int)(row % p.T), head = (int)(row / p.T % p.H), b = (int)(row / p.T / p.H);
-  const int h = head / (p.H / p.c.Hkv);
-  const int n = kv4_count(p.c, b, p.T);
-  const long long start = p.c.start[b];
-  long long keys = t >= n ? 0 : p.causal ? start + t + 1 : start + n;
-  // lane owns elements lane*W .. lane*W + W - 1, all in one group
-  float q[W], o[W], m = -INFINITY, l = 0.f;
-  const uint16_t* qr = static_cast<const uint16_t*>(p.q) + row * D + lane * W;
-#pragma unroll
-  for (int i = 0; i < W; ++i) {
-    q[i] = kv4_scale<BF16>(qr[i]) * p.scale_log2;
-    o[i] = 0.f;
+
+  // ---- how many steps there are, and which of them are this warp's
+  const int per = (p.B + kThreads - 1) / kThreads;
+  long long mine = 0;
+  for (int i = 0, b = threadIdx.x * per; i < per && b < p.B; ++i, ++b) {
+    const Reach r = reach(p, b);
+    mine += r.steps;
+    if (blockIdx.x == 0 && r.n > 0 && r.start + r.n > r.keys && r.start + r.n > 0)   // past the page table
+      atomicCAS(p.c.status, 0, FA_ERR_PAGE);
   }
-  for (long long j = warp; j < keys; j += NW) {
-    const uint8_t* blk = kv4_block_of(p.c, b, h, j, kv4_block_bytes(D));
-    if (blk == nullptr) continue;
-    const int key = (int)j & 15, half = key >> 3, e0 = lane * W, grp = e0 / 32;
-    const uint16_t* sc = reinterpret_cast<const uint16_t*>(blk + 16 * D) + key * 2 * W + grp;
-    const uint32_t kw = reinterpret_cast<const uint32_t*>(blk)[((half * 8 + (key & 7)) * 4 + e0 % 32 / 8) * W + grp];
-    const int r = e0 / (D / 8), w = e0 % (D / 8) / 4;
-    const uint32_t vw =
-        reinterpret_cast<const uint32_t*>(blk + 8 * D)[((half * 8 + r) * 4 + ((key & 7) >> 1)) * W + w];
-    const uint32_t kh = (kw >> (e0 % 8 / 4 * 16)) & 0xffffu, vh = (vw >> ((key & 1) * 16)) & 0xffffu;
-    const uint32_t kn = ((kh >> 2) | (kh << 14)) & 0xffffu, vn = ((vh >> 2) | (vh << 14)) & 0xffffu;
-    const float sk = kv4_scale<BF16>(sc[0]), sv = kv4_scale<BF16>(sc[W]);
-    float s = 0.f;
+  mine *= p.units_per_seq;
+  long long incl = mine;
 #pragma unroll
-    for (int i = 0; i < W; ++i) s = fmaf(q[i], (float)((int)((kn >> (4 * (e0 % 4 + i))) & 15u) - 8), s);
-    s *= sk;
-#pragma unroll
-    for (int d = 16; d; d >>= 1) s += __shfl_xor_sync(0xffffffffu, s, d);
-    const float mn = fmaxf(m, s), f = m == -INFINITY ? 0.f : exp2f(m - mn), pj = exp2f(s - mn);
-    l = l * f + pj;
-    m = mn;
-#pragma unroll
-    for (int i = 0; i < W; ++i)
-      o[i] = o[i] * f + pj * (sv * (float)((int)((vn >> (4 * (e0 % 4 + i))) & 15u) - 8));
+  for (int d = 1; d < 32; d *= 2) {
+    const long long o = __shfl_up_sync(0xffffffffu, incl, d);
+    if (lane >= d) incl += o;
   }
-  __shared__ float sm[NW], sl[NW], so[NW][D];
-  if (lane == 0) sm[warp] = m, sl[warp] = l;
-#pragma unroll
-  for (int i = 0; i < W; ++i) so[warp][lane * W + i] = o[i];
+  if (lane == 31) warp_sum[warp] = incl;
   __syncthreads();
-  if (threadIdx.x < D) {
-    float mm = -INFINITY, ll = 0.f, oo = 0.f;
-    for (int k = 0; k < NW; ++k) mm = fmaxf(mm, sm[k]);
-    for (int k = 0; k < NW; ++k) {
-      const float f = sm[k] == -INFINITY ? 0.f : exp2f(sm[k] - mm);
-      ll += f * sl[k];
-      oo += f * so[k][threadIdx.x];
-    }
-    oo = ll == 0.f ? 0.f : oo / ll;
-    const long long at = row * D + threadIdx.x;
-    if constexpr (O32)
-      static_cast<float*>(p.o)[at] = oo;
-    else if constexpr (BF16)
-      static_cast<__nv_bfloat16*>(p.o)[at] = __float2bfloat16_rn(oo);
-    else
-      static_cast<__half*>(p.o)[at] = __float2half_rn(oo);
-    if (threadIdx.x == 0) p.lse[row] = (mm + log2f(ll)) * 0.69314718055994531f;
+  long long before = 0, total = 0;
+#pragma unroll
+  for (int i = 0; i < kWarps; ++i) {
+    if (i < warp) before += warp_sum[i];
+    total += warp_sum[i];
   }
+  chunk_sum[threadIdx.x] = before + incl - mine;
+  __syncthreads();
+
+  const long long workers = (long long)gridDim.x * kWarps, worker = (long long)blockIdx.x * kWarps + warp;
+  long long each = (total + workers - 1) / workers;
+  if (each < kMinSteps) each = kMinSteps;
+  const long long lo = worker * each, hi = lo + each < total ? lo + each : total;
+  if (lo >= hi) {
+    if (lane == 0) p.joins[worker].parts = 0;
+    return;
+  }
+  const long long todo = hi - lo;
+
+  int first = 0;   // the last chunk that does not begin behind lo
+#pragma unroll
+  for (int i = 0; i < kThreads / 32; ++i) first += __popc(__ballot_sync(0xffffffffu, chunk_sum[32 * i + lane] <= lo));
+  --first;
+  Cursor at;
+  at.b = first * per;
+  at.rem = lo - chunk_sum[first];
+  at.r = reach(p, at.b);
+  at.settle(p);
+
+  // ---- the producer: lane i looks up block i % 2 of step 16 k + i / 2
+  Cursor next = at;
+  next.rem += lane / 2;
+  long long ahead = lane / 2;   // the step that `next` stands on, counted from lo
+  int page_next = -1, in_page_next = 0;
+  const int per_page_shift = p.c.page_shift - 4;
+  auto look_up = [&]() {
+    page_next = -2;   // no such block: nothing to copy
+    next.settle(p);
+    if (ahead < todo) {
+      const unsigned u = (unsigned)((unsigned long long)next.rem / (unsigned)next.r.steps);
+      const int blk = 2 * (int)(next.rem - (long long)u * next.r.steps) + (lane & 1);
+      if ((long long)blk * kKv4Block < next.r.keys) {
+        page_next = p.c.table[(size_t)next.b * p.c.max_pages + (size_t)(blk >> per_page_shift)];
+        if (page_next < 0) page_next = -1;
+        in_page_next = (int)((u / p.row_tiles) << per_page_shift) + (blk & ((1 << per_page_shift) - 1));
+      }
+    }
+    ahead += kBatch;
+    next.rem += kBatch;
+  };
+  const uint8_t* src = nullptr;
+  uint32_t have = 0, have_before = 0;   // which blocks of this batch and of the one before exist
+  long long made = 0;
+  auto produce = [&]() {
+    if (made % kBatch == 0) {
+      const bool ok = page_next >= 0 && page_next < p.c.n_pages;
+      if (!ok && page_next != -2) atomicCAS(p.c.status, 0, FA_ERR_PAGE);
+      src = ok ? p.c.pool + (((size_t)page_next * p.c.Hkv << per_page_shift) + in_page_next) * (size_t)Block : nullptr;
+      have_before = have;
+      have = __ballot_sync(0xffffffffu, ok);
+      look_up();
+    }
+    if (lane / 2 == (int)(made % kBatch)) {
+      const int slot = (int)(made % ST);
+      if (src != nullptr) {
+        mbar_arrive_expect_tx(bar0 + 8 * slot, Block);
+        bulk_load(ring0 + (slot * 2 + (lane & 1)) * Block, src, Block, bar0 + 8 * slot);
+      } else {
+        mbar_arrive(bar0 + 8 * slot);
+      }
+    }
+    ++made;
+  };
+  look_up();
+  while (made < todo && made < ST) produce();
+
+  const WaitCtx wc{p.wait_limit_ns, &abort_flag, p.c.status};
+  Kv4Join join{0, 0, 0};
+  const int group = p.H / p.c.Hkv;
+  const long long unit_rows = (long long)group * p.T;
+  long long done = 0;
+  bool alive = true;
+
+  while (done < todo && alive) {
+    // ---- one unit's share
+    const Reach r = at.r;
+    const unsigned u = (unsigned)((unsigned long long)at.rem / (unsigned)r.steps);
+    const int s0 = (int)(at.rem - (long long)u * r.steps);
+    const long long left = todo - done;
+    const int s1 = (long long)(r.steps - s0) < left ? r.steps : s0 + (int)left;
+    const int h = (int)(u / p.row_tiles), tile = (int)(u - (unsigned)h * p.row_tiles);
+    const long long row_in = (long long)tile * Sh::Rows;
+    const long long row0 = ((long long)at.b * p.H + (long long)h * group) * p.T + row_in;
+    const int rows = unit_rows - row_in < Sh::Rows ? (int)(unit_rows - row_in) : Sh::Rows;
+
+    uint32_t qb[NT][W][4];
+    float init[NT][W][2], f[NT][W][2];
+    int lim[NT][2];
+    int full_end = 0x7fffffff, last_key = 0;
+    const long long cap = (long long)p.c.max_pages << p.c.page_shift;
+    auto limit_of = [&](int row) -> int {
+      if (row >= rows) return 0;
+      const int tok = (int)(((unsigned)row_in + row) % (unsigned)p.T);
+      if (tok >= r.n) return 0;
+      const long long e = p.causal ? r.start + tok + 1 : r.start + r.n;
+      return (int)(e < 0 ? 0 : e > cap ? cap : e);
+    };
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) {
+      const int my_lim = limit_of(8 * nt + g);
+      const uint4* qr = reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(p.q) + (row0 + 8 * nt + g) * D) + t;
+#pragma unroll
+      for (int e = 0; e < W; ++e) {
+        uint4 x = make_uint4(0, 0, 0, 0);
+        if (my_lim > 0) x = qr[4 * e];
+        float v[8];
+        const uint32_t xs[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          v[2 * i] = kv4_scale<BF16>((uint16_t)(xs[i] & 0xffffu));
+          v[2 * i + 1] = kv4_scale<BF16>((uint16_t)(xs[i] >> 16));
+        }
+        float back = p.scale_log2;
+        if constexpr (BF16) {
+          float top = 0.f;
+#pragma unroll
+          for (int i = 0; i < 8; ++i) top = fmaxf(top, fabsf(v[i]));
+          top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
+          top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
+          int ex = 14 + 127 - (int)(__float_as_uint(top) >> 23);   // top * 2^ex in [2^14, 2^15)
+          ex = ex > 100 ? 100 : ex;
+          const float up = pow2(ex);
+          back = p.scale_log2 * pow2(-ex);
+#pragma unroll
+          for (int i = 0; i < 8; ++i) v[i] *= up;
+        }
+        float even = 0.f, odd = 0.f;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          qb[nt][e][i] = pack2<false>(v[i], v[i + 4]);
+          const float2 y = __half22float2(*reinterpret_cast<__half2*>(&qb[nt][e][i]));
+          (i & 1 ? odd : even) += y.x + y.y;
+        }
+        float c = -(264.f * even + 24.f * odd);
+        c += __shfl_xor_sync(0xffffffffu, c, 1);
+        c += __shfl_xor_sync(0xffffffffu, c, 2);
+        init[nt][e][0] = __shfl_sync(0xffffffffu, c, 8 * t);
+        init[nt][e][1] = __shfl_sync(0xffffffffu, c, 8 * t + 4);
+        f[nt][e][0] = __shfl_sync(0xffffffffu, back, 8 * t);
+        f[nt][e][1] = __shfl_sync(0xffffffffu, back, 8 * t + 4);
+      }
+      if (my_lim > 0) full_end = min(full_end, my_lim);
+      last_key = max(last_key, my_lim);
+      lim[nt][0] = __shfl_sync(0xffffffffu, my_lim, 8 * t);
+      lim[nt][1] = __shfl_sync(0xffffffffu, my_lim, 8 * t + 4);
+    }
+    full_end = __reduce_min_sync(0xffffffffu, full_end);
+    last_key = __reduce_max_sync(0xffffffffu, last_key);
+
+    float o[NT][W][2][4], m[NT][2], m_pass[NT][2], l[NT][2];
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) {
+#pragma unroll
+      for (int e = 0; e < W; ++e)
+#pragma unroll
+        for (int i = 0; i < 8; ++i) o[nt][e][i / 4][i % 4] = 0.f;
+#pragma unroll
+      for (int c = 0; c < 2; ++c) m[nt][c] = 0.f, m_pass[nt][c] = -INFINITY, l[nt][c] = 0.f;
+    }
+    float v_up = 1.f, v_pass = 0.f;   // s_V goes in times v_up, and may reach v_pass
+
+    for (int s = s0; s < s1; ++s, ++done) {
+      const int slot = (int)(done % ST);
+      alive = warp_all(mbar_wait(bar0 + 8 * slot, (uint32_t)(done / ST) & 1u, wc));
+      if (!alive) break;
+      const uint32_t which = (done / kBatch == (made - 1) / kBatch ? have : have_before) >> (2 * (int)(done % kBatch)) & 3u;
+      const long long key0 = (long long)s * kStep;
+      if (which != 0 && key0 < last_key) {
+        const uint8_t* const base = ring + slot * 2 * Block;
+        float sc[NT][2][4], sv[2][2][W];
+#pragma unroll
+        for (int bk = 0; bk < 2; ++bk) {
+          const uint8_t* blk = base + bk * Block;
+          float sk[2][W];
+          uint32_t kw[2][W];
+#pragma unroll
+          for (int half = 0; half < 2; ++half) {
+            uint32_t raw[W];
+            if constexpr (W == 4) {
+              const uint4 x = reinterpret_cast<const uint4*>(blk)[half * 32 + lane];
+              kw[half][0] = x.x, kw[half][1] = x.y, kw[half][2] = x.z, kw[half][3] = x.w;
+              const uint4 y = reinterpret_cast<const uint4*>(blk + 16 * D)[half * 8 + g];
+              raw[0] = y.x, raw[1] = y.y, raw[2] = y.z, raw[3] = y.w;
+            } else {
+              const uint2 x = reinterpret_cast<const uint2*>(blk)[half * 32 + lane];
+              kw[half][0] = x.x, kw[half][1] = x.y;
+              const uint2 y = reinterpret_cast<const uint2*>(blk + 16 * D)[half * 8 + g];
+              raw[0] = y.x, raw[1] = y.y;
+            }
+#pragma unroll
+            for (int e = 0; e < W; ++e) {
+              sk[half][e] = kv4_scale<BF16>((uint16_t)(raw[e / 2] >> (16 * (e & 1))));
+              sv[bk][half][e] = kv4_scale<BF16>((uint16_t)(raw[W / 2 + e / 2] >> (16 * (e & 1))));
+            }
+          }
+#pragma unroll
+          for (int e = 0; e < W; ++e) {
+            const uint32_t x0 = kw[0][e], x1 = kw[1][e];
+            const uint32_t y0 = __byte_perm(x0, 0, 0x2301), y1 = __byte_perm(x1, 0, 0x2301);
+            const uint32_t a0[4] = {(x0 & 0x003c003cu) | 0x5c005c00u, (x1 & 0x003c003cu) | 0x5c005c00u,
+                                    (x0 & 0x03c003c0u) | 0x4c004c00u, (x1 & 0x03c003c0u) | 0x4c004c00u};
+            const uint32_t a1[4] = {(y0 & 0x003c003cu) | 0x5c005c00u, (y1 & 0x003c003cu) | 0x5c005c00u,
+                                    (y0 & 0x03c003c0u) | 0x4c004c00u, (y1 & 0x03c003c0u) | 0x4c004c00u};
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt) {
+              const float c[4] = {init[nt][e][0], init[nt][e][1], init[nt][e][0], init[nt][e][1]};
+              float d[4];
+              mma16816(d, a0, qb[nt][e][0], qb[nt][e][1], c);
+              mma16816(d, a1, qb[nt][e][2], qb[nt][e][3], d);
+#pragma unroll
+              for (int i = 0; i < 4; ++i) {
+                const float x = BF16 ? d[i] * f[nt][e][i & 1] : d[i];
+                sc[nt][bk][i] = e == 0 ? x * sk[i / 2][0] : fmaf(x, sk[i / 2][e], sc[nt][bk][i]);
+              }
+            }
+          }
+        }
+        if constexpr (!BF16) {
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+            for (int i = 0; i < 8; ++i) sc[nt][i / 4][i % 4] *= f[nt][0][i & 1];
+        }
+        if (which != 3u || key0 + kStep > full_end) {
+          // keys that a row does not see; scales behind the last key may be anything
+#pragma unroll
+          for (int bk = 0; bk < 2; ++bk)
+#pragma unroll
+            for (int half = 0; half < 2; ++half) {
+              const long long key = key0 + 16 * bk + 8 * half + g;
+              const bool there = (which >> bk & 1u) != 0;
+              if (!there || key >= last_key) {
+#pragma unroll
+                for (int e = 0; e < W; ++e) sv[bk][half][e] = 0.f;
+              }
+#pragma unroll
+              for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                for (int c = 0; c < 2; ++c)
+                  if (!there || key >= lim[nt][c]) sc[nt][bk][2 * half + c] = -INFINITY;
+            }
+        }
+        // ---- V's scales, relative to the largest so far
+        float v_top = 0.f;
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+#pragma unroll
+          for (int e = 0; e < W; e += 2)
+            v_top = fmax3(v_top, fabsf(sv[i / 2][i % 2][e]), fabsf(sv[i / 2][i % 2][e + 1]));
+        bool pass = v_top > v_pass;
+        float top[NT][2];
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+          for (int c = 0; c < 2; ++c) {
+            top[nt][c] = fmaxf(fmax3(sc[nt][0][c], sc[nt][0][2 + c], sc[nt][1][c]), sc[nt][1][2 + c]);
+            pass = pass || top[nt][c] > m_pass[nt][c];
+          }
+        if (__any_sync(0xffffffffu, pass)) {
+          float all = v_top;
+#pragma unroll
+          for (int d = 16; d; d /= 2) all = fmaxf(all, __shfl_xor_sync(0xffffffffu, all, d));
+          float fv = 1.f;
+          if (all > v_pass) {
+            int ex = (int)(__float_as_uint(all) >> 23) - 127;
+            ex = ex < -114 ? -114 : ex;
+            const float up = pow2(6 - ex);
+            fv = v_pass == 0.f ? 0.f : up / v_up;   // nothing to scale before the first value
+            v_up = up;
+            v_pass = pow2(ex) * 2.f;
+          }
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+            for (int c = 0; c < 2; ++c) {
+              const float mx = quad_max(top[nt][c]);
+              float fm = 1.f;
+              if (mx > m_pass[nt][c]) {
+                fm = m_pass[nt][c] == -INFINITY ? 0.f : ex2_approx(m[nt][c] - mx);
+                m[nt][c] = mx;
+                m_pass[nt][c] = mx + kLazy;
+                l[nt][c] *= fm;
+              }
+#pragma unroll
+              for (int i = 0; i < 2 * W; ++i) {
+                o[nt][i / 2][i % 2][c] *= fm * fv;
+                o[nt][i / 2][i % 2][2 + c] *= fm * fv;
+              }
+            }
+        }
+#pragma unroll
+        for (int i = 0; i < 4 * W; ++i) sv[i / (2 * W)][i / W % 2][i % W] *= v_up;
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+          for (int i = 0; i < 8; ++i) {
+            float& x = sc[nt][i / 4][i % 4];
+            x = ex2_approx(x - m[nt][i & 1]);
+            l[nt][i & 1] += x;
+          }
+        // ---- O^T += V^T P^T
+#pragma unroll
+        for (int bk = 0; bk < 2; ++bk) {
+          const uint8_t* blk = base + bk * Block + 8 * D;
+          uint32_t vw[2][W];
+#pragma unroll
+          for (int half = 0; half < 2; ++half) {
+            if constexpr (W == 4) {
+              const uint4 x = reinterpret_cast<const uint4*>(blk)[half * 32 + lane];
+              vw[half][0] = x.x, vw[half][1] = x.y, vw[half][2] = x.z, vw[half][3] = x.w;
+            } else {
+              const uint2 x = reinterpret_cast<const uint2*>(blk)[half * 32 + lane];
+              vw[half][0] = x.x, vw[half][1] = x.y;
+            }
+          }
+#pragma unroll
+          for (int e = 0; e < W; ++e) {
+            const uint32_t x0 = vw[0][e], x1 = vw[1][e];
+            const uint32_t y0 = __byte_perm(x0, 0, 0x2301), y1 = __byte_perm(x1, 0, 0x2301);
+            const uint32_t a0[4] = {hsub2((x0 & 0x003c003cu) | 0x5c005c00u, 0x5c205c20u),
+                                    hsub2((x0 & 0x03c003c0u) | 0x4c004c00u, 0x4e004e00u),
+                                    hsub2((x1 & 0x003c003cu) | 0x5c005c00u, 0x5c205c20u),
+                                    hsub2((x1 & 0x03c003c0u) | 0x4c004c00u, 0x4e004e00u)};
+            const uint32_t a1[4] = {hsub2((y0 & 0x003c003cu) | 0x5c005c00u, 0x5c205c20u),
+                                    hsub2((y0 & 0x03c003c0u) | 0x4c004c00u, 0x4e004e00u),
+                                    hsub2((y1 & 0x003c003cu) | 0x5c005c00u, 0x5c205c20u),
+                                    hsub2((y1 & 0x03c003c0u) | 0x4c004c00u, 0x4e004e00u)};
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt) {
+              const float(&pr)[4] = sc[nt][bk];
+              const uint32_t b0 = transpose8x8(pack2<false>(pr[0] * sv[bk][0][e], pr[1] * sv[bk][0][e]));
+              const uint32_t b1 = transpose8x8(pack2<false>(pr[2] * sv[bk][1][e], pr[3] * sv[bk][1][e]));
+              mma16816(o[nt][e][0], a0, b0, b1, o[nt][e][0]);
+              mma16816(o[nt][e][1], a1, b0, b1, o[nt][e][1]);
+            }
+          }
+        }
+      }
+      __syncwarp();
+      if (made < todo) produce();
+    }
+    if (!alive) break;
+
+    // ---- the unit's result, or this warp's piece of it
+    const bool begins = s0 == 0, ends = s1 == r.steps;
+    float* const part = begins && ends ? nullptr : slot_of(p, worker, begins ? 1 : 0, Sh::Slot);
+    const float v_down = v_pass == 0.f ? 0.f : 1.f / v_up;
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+      for (int c = 0; c < 2; ++c) {
+        const int row = 8 * nt + 2 * t + c;
+        float ll = quad_sum(l[nt][c]), mm = m_pass[nt][c] == -INFINITY ? -INFINITY : m[nt][c];
+        if (row >= rows) continue;
+        if (lim[nt][c] == 0) ll = 0.f, mm = -INFINITY;   // steps that all other rows see whole do not mask this one
+        const float inv = ll == 0.f ? 0.f : 1.f / ll;
+#pragma unroll
+        for (int e = 0; e < W; ++e) {
+          const float4 x = make_float4(o[nt][e][0][c] * inv * v_down, o[nt][e][0][2 + c] * inv * v_down,
+                                       o[nt][e][1][c] * inv * v_down, o[nt][e][1][2 + c] * inv * v_down);
+          const int col = 32 * e + 4 * g;
+          if (part != nullptr)
+            *reinterpret_cast<float4*>(part + row * D + col) = x;
+          else if (p.o32)
+            *reinterpret_cast<float4*>(static_cast<float*>(p.o) + (row0 + row) * D + col) = x;
+          else
+            *reinterpret_cast<uint2*>(static_cast<uint16_t*>(p.o) + (row0 + row) * D + col) =
+                make_uint2(pack2<BF16>(x.x, x.y), pack2<BF16>(x.z, x.w));
+        }
+        if (g == 0) {
+          if (part != nullptr)
+            *reinterpret_cast<float2*>(part + Sh::Rows * D + 2 * row) = make_float2(mm, ll);
+          else
+            p.lse[row0 + row] = (mm + log2f(ll)) * 0.69314718055994531f;
+        }
+      }
+    if (begins && !ends) {
+      join.row = row0;
+      join.rows = rows;
+      join.parts = (int)((r.steps - s1 + each - 1) / each);
+    }
+    at.rem += s1 - s0;
+    at.settle(p);
+  }
+  if (!alive) {
+    // copies in flight land before the CTA's shared memory goes
+    for (; done < made; ++done)
+      if (!warp_all(mbar_wait_drain(bar0 + 8 * (int)(done % ST), (uint32_t)(done / ST) & 1u, p.wait_limit_ns))) break;
+    join.parts = 0;
+  }
+  if (lane == 0) p.joins[worker] = join;
+}
+
+// O and LSE of the units that lie across workers: one CTA for each worker in
+// which such a unit begins.  Pieces are normalised, with their maximum m (in
+// log2) and sum l beside them; a piece that saw no key has m = -inf, l = 0.
+template <bool BF16, int D, int NT>
+__global__ void __launch_bounds__(256) fa_kv4_join_kernel(const Kv4FwdParams p) {
+  using Sh = Shape<D, NT>;
+  grid_dependency_wait();
+  grid_dependents_launch();
+  const long long worker = blockIdx.x;
+  const Kv4Join j = p.joins[worker];
+  if (j.parts == 0) return;
+  for (int i = threadIdx.x; i < j.rows * (D / 4); i += 256) {
+    const int row = i / (D / 4), col = 4 * (i % (D / 4));
+    float mm = -INFINITY, ll = 0.f;
+    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 4
+    for (int k = 0; k <= j.parts; ++k) {
+      const float* part = slot_of(p, worker + k, k == 0 ? 1 : 0, Sh::Slot);
+      const float2 ml = *reinterpret_cast<const float2*>(part + Sh::Rows * D + 2 * row);
+      const float4 x = *reinterpret_cast<const float4*>(part + row * D + col);
+      const float mn = fmaxf(mm, ml.x);
+      const float fa = mm == -INFINITY ? 1.f : ex2_approx(mm - mn);             // ll and acc are 0 or NaN while mm is -inf
+      const float fb = ml.x == -INFINITY ? ml.y : ml.y * ex2_approx(ml.x - mn);
+      ll = ll * fa + fb;
+      acc.x = acc.x * fa + x.x * fb, acc.y = acc.y * fa + x.y * fb;
+      acc.z = acc.z * fa + x.z * fb, acc.w = acc.w * fa + x.w * fb;
+      mm = mn;
+    }
+    const float inv = ll == 0.f ? 0.f : 1.f / ll;
+    acc.x *= inv, acc.y *= inv, acc.z *= inv, acc.w *= inv;
+    const long long at = (j.row + row) * D + col;
+    if (p.o32)
+      *reinterpret_cast<float4*>(static_cast<float*>(p.o) + at) = acc;
+    else
+      *reinterpret_cast<uint2*>(static_cast<uint16_t*>(p.o) + at) =
+          make_uint2(pack2<BF16>(acc.x, acc.y), pack2<BF16>(acc.z, acc.w));
+    if (col == 0) p.lse[j.row + row] = (mm + log2f(ll)) * 0.69314718055994531f;
+  }
+}
+
+constexpr int kMaxSms = 160;
+
+// Query rows of a unit, in tiles of 8: what K's and V's decoding is shared by.
+int row_tiles_of(int d, long long rows) { return rows <= 8 ? 1 : rows <= 16 || d == 128 ? 2 : 4; }
+
+template <bool BF16, int D, int NT>
+cudaError_t launch(Kv4FwdParams p, void* workspace, int sms, cudaStream_t st) {
+  using Sh = Shape<D, NT>;
+  const long long rows = (long long)(p.H / p.c.Hkv) * p.T;
+  p.row_tiles = (int)((rows + Sh::Rows - 1) / Sh::Rows);
+  p.units_per_seq = (long long)p.c.Hkv * p.row_tiles;
+  const int grid = (sms < kMaxSms ? sms : kMaxSms) * Sh::CtasPerSm;
+  p.joins = static_cast<Kv4Join*>(workspace);
+  p.partials = reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + sizeof(Kv4Join) * kMaxSms * kWarps * 3);
+  auto kern = fa_kv4_fwd_kernel<BF16, D, NT>;
+  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)Sh::Smem);
+  if (e != cudaSuccess) return e;
+  if ((e = launch_chained(kern, dim3(grid), dim3(kThreads), Sh::Smem, st, p)) != cudaSuccess) return e;
+  return launch_chained(fa_kv4_join_kernel<BF16, D, NT>, dim3(grid * kWarps), dim3(256), 0, st, p);
 }
 
 }  // namespace
 
-cudaError_t launch_kv4_fwd(bool bf16, bool o32, int d, const Kv4FwdParams& p, cudaStream_t st) {
-  const dim3 grid((unsigned)((long long)p.B * p.H * p.T));
-#define FA_KV4(BB, DD) \
-  (o32 ? launch_chained(fa_kv4_fwd_kernel<BB, DD, true>, grid, dim3(kThreads), 0, st, p) \
-       : launch_chained(fa_kv4_fwd_kernel<BB, DD, false>, grid, dim3(kThreads), 0, st, p))
-  if (bf16) return d == 64 ? FA_KV4(true, 64) : FA_KV4(true, 128);
-  return d == 64 ? FA_KV4(false, 64) : FA_KV4(false, 128);
+size_t kv4_fwd_workspace(int d, long long rows) {
+  const int nt = row_tiles_of(d, rows), ctas = d / 32 * nt <= 4 ? 3 : 2;
+  return sizeof(Kv4Join) * kMaxSms * kWarps * 3 + (size_t)kMaxSms * ctas * kWarps * 2 * (8 * nt) * (d + 2) * 4;
+}
+
+cudaError_t launch_kv4_fwd(bool bf16, int d, const Kv4FwdParams& p, void* workspace, int sms, cudaStream_t st) {
+  const int nt = row_tiles_of(d, (long long)(p.H / p.c.Hkv) * p.T);
+#define FA_KV4(DD, NN) \
+  (bf16 ? launch<true, DD, NN>(p, workspace, sms, st) : launch<false, DD, NN>(p, workspace, sms, st))
+  if (d == 128) return nt == 1 ? FA_KV4(128, 1) : FA_KV4(128, 2);
+  return nt == 1 ? FA_KV4(64, 1) : nt == 2 ? FA_KV4(64, 2) : FA_KV4(64, 4);
 #undef FA_KV4
 }
 
