@@ -116,7 +116,7 @@ __device__ __forceinline__ uint32_t quantise8(uint4 x, uint16_t* s16) {
     // sum of c_i 16^i; what the 0x4b of each float leaves is above bit 23
     half[j] = c[0] + (c[1] << 4) + (c[2] << 8) + (c[3] << 12);
   }
-  return kv4_rotl16x2(__byte_perm(half[0], half[1], 0x5410));
+  return __byte_perm(half[0], half[1], 0x5410);
 }
 
 struct WriteParams {
@@ -180,8 +180,7 @@ __global__ void __launch_bounds__(kThreads) fa_kv4_write_kernel(const WriteParam
 
 // Eight codes (a word of two half-words) times s, in the 16-bit type.
 template <bool BF16>
-__device__ __forceinline__ uint4 values8(uint32_t word, float s) {
-  const uint32_t w = ((word >> 2) & 0x3fff3fffu) | ((word << 14) & 0xc000c000u);
+__device__ __forceinline__ uint4 values8(uint32_t w, float s) {
   uint32_t r[4];
 #pragma unroll
   for (int j = 0; j < 4; ++j) {

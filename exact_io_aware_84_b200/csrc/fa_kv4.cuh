@@ -20,12 +20,11 @@
 // code moves between lanes.  A half-word belongs to one key, so writing a
 // token touches no byte of another one.
 //
-// A half-word's four codes c = n + 8 lie at bits 2..5, 6..9, 10..13 and
-// {14,15,0,1} (nibbles in order, rotated left by 2).  Under the masks 0x003c
-// and 0x03c0 a code falls into an fp16 mantissa as it stands: with the
-// exponent bits 0x5c00 it reads 256 + c, with 0x4c00 it reads 16 + c.
-// Swapping the bytes of each half-word brings the other two codes to the same
-// places: 5 integer instructions for 8 codes.
+// A half-word's four codes c = n + 8 are its nibbles in order.  Under the
+// masks 0x000f and 0x00f0 a code is an fp16 subnormal as it stands, c 2^-24 or
+// c 2^-20, which the tensor cores multiply exactly; the word shifted right by
+// 8 brings the other two codes to the same places: 5 integer instructions for
+// 8 codes.
 #pragma once
 
 #include <cuda_bf16.h>
@@ -42,11 +41,6 @@ constexpr int kKv4Group = 32;   // elements that share a scale
 constexpr int kKv4Block = 16;   // tokens of a block
 
 __host__ __device__ constexpr int kv4_block_bytes(int d) { return 18 * d; }
-
-// Both half-words rotated left by 2.
-__device__ __forceinline__ uint32_t kv4_rotl16x2(uint32_t w) {
-  return ((w << 2) & 0xfffcfffcu) | ((w >> 14) & 0x00030003u);
-}
 
 // Tokens of sequence b in this call: count clamped to [0, T].
 __device__ __forceinline__ int kv4_count(const Kv4Cache& c, int b, int T) {

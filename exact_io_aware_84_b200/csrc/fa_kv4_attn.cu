@@ -16,12 +16,11 @@
 // ring that belongs to the warp, ST steps deep, so no warp waits for another.
 //   S^T = K Q^T by mma.m16n8k16, keys as rows and 8 query rows as columns:
 //     nothing is wasted when four or eight query heads share a key head.  A
-//     code's nibble enters an fp16 mantissa (256 + c and 16 + c); the offsets
-//     are taken back by starting each group's sum at -264 or -24 times q's.
-//     The sum over a group of 32 is scaled in float32.  q goes in as fp16: a
-//     bf16 q is brought to 2^14 .. 2^15 per row and group by a power of two,
-//     which the scale takes back (elements 2^31 below the group's largest
-//     round, relative to it, at 2^-40).
+//     code c = n + 8 enters as the fp16 subnormal that its nibble is, and 8
+//     times the sum of q is taken off each group's sum of 32, which is then
+//     scaled in float32.  q goes in as fp16, brought to 2^14 .. 2^15 per row
+//     and group by a power of two that the scale takes back (elements 2^21
+//     below the group's largest round, relative to it, at 2^-36).
 //   O^T = V^T P^T: the head's elements as rows.  V's codes become n by one
 //     fp16 subtraction (exact: a sum over many keys must not carry an offset);
 //     P s_V is rounded to fp16, with s_V taken relative to the largest one so
@@ -53,6 +52,7 @@ constexpr int kThreads = 32 * kWarps;
 constexpr int kStep = 32;               // keys of a step: two blocks
 constexpr int kBatch = 16;              // steps whose pages a warp looks up at once
 constexpr int kMinSteps = 2;            // least steps worth a warp
+constexpr float kUnit = 16777216.f;     // scores and O are summed in units of 2^-24, the subnormals' step
 constexpr float kLazy = 8.f;            // log2 by which a score may pass the running maximum
 
 template <int D, int NT>
@@ -223,44 +223,51 @@ __global__ void __launch_bounds__(kThreads, (Shape<D, NT>::CtasPerSm)) fa_kv4_fw
     next.rem += kBatch;
   };
   const uint8_t* src = nullptr;
-  uint32_t have = 0, have_before = 0;   // which blocks of this batch and of the one before exist
-  long long made = 0;
+  uint32_t have = 0;              // which blocks of this batch exist
+  long long to_make = todo;
+  int make_at = 0, make_slot = 0;   // the step's place in its batch and in the ring
   auto produce = [&]() {
-    if (made % kBatch == 0) {
+    if (make_at == 0) {
       const bool ok = page_next >= 0 && page_next < p.c.n_pages;
       if (!ok && page_next != -2) atomicCAS(p.c.status, 0, FA_ERR_PAGE);
       src = ok ? p.c.pool + (((size_t)page_next * p.c.Hkv << per_page_shift) + in_page_next) * (size_t)Block : nullptr;
-      have_before = have;
       have = __ballot_sync(0xffffffffu, ok);
       look_up();
     }
-    if (lane / 2 == (int)(made % kBatch)) {
-      const int slot = (int)(made % ST);
+    if (lane / 2 == make_at) {
+      const uint32_t bar = bar0 + 8 * make_slot;
       if (src != nullptr) {
-        mbar_arrive_expect_tx(bar0 + 8 * slot, Block);
-        bulk_load(ring0 + (slot * 2 + (lane & 1)) * Block, src, Block, bar0 + 8 * slot);
+        mbar_arrive_expect_tx(bar, Block);
+        bulk_load(ring0 + (make_slot * 2 + (lane & 1)) * Block, src, Block, bar);
       } else {
-        mbar_arrive(bar0 + 8 * slot);
+        mbar_arrive(bar);
       }
     }
-    ++made;
+    make_at = (make_at + 1) % kBatch;
+    make_slot = (make_slot + 1) % ST;
+    --to_make;
   };
   look_up();
-  while (made < todo && made < ST) produce();
+#pragma unroll
+  for (int i = 0; i < ST; ++i)
+    if (to_make > 0) produce();
 
   const WaitCtx wc{p.wait_limit_ns, &abort_flag, p.c.status};
   Kv4Join join{0, 0, 0};
   const int group = p.H / p.c.Hkv;
   const long long unit_rows = (long long)group * p.T;
-  long long done = 0;
+  long long left = todo;
+  uint32_t exist = 0;                          // as `have`, from the step to come on
+  int take_at = 0, take_slot = 0;              // as make_at and make_slot
+  uint32_t phase = 0;
   bool alive = true;
+  int flying = 0;                              // steps on their way when a wait ran out
 
-  while (done < todo && alive) {
+  while (left > 0 && alive) {
     // ---- one unit's share
     const Reach r = at.r;
     const unsigned u = (unsigned)((unsigned long long)at.rem / (unsigned)r.steps);
     const int s0 = (int)(at.rem - (long long)u * r.steps);
-    const long long left = todo - done;
     const int s1 = (long long)(r.steps - s0) < left ? r.steps : s0 + (int)left;
     const int h = (int)(u / p.row_tiles), tile = (int)(u - (unsigned)h * p.row_tiles);
     const long long row_in = (long long)tile * Sh::Rows;
@@ -268,7 +275,7 @@ __global__ void __launch_bounds__(kThreads, (Shape<D, NT>::CtasPerSm)) fa_kv4_fw
     const int rows = unit_rows - row_in < Sh::Rows ? (int)(unit_rows - row_in) : Sh::Rows;
 
     uint32_t qb[NT][W][4];
-    float init[NT][W][2], f[NT][W][2];
+    float take[NT][W][2], f[NT][W][2];   // of the rows of this lane's columns
     int lim[NT][2];
     int full_end = 0x7fffffff, last_key = 0;
     const long long cap = (long long)p.c.max_pages << p.c.page_shift;
@@ -294,32 +301,27 @@ __global__ void __launch_bounds__(kThreads, (Shape<D, NT>::CtasPerSm)) fa_kv4_fw
           v[2 * i] = kv4_scale<BF16>((uint16_t)(xs[i] & 0xffffu));
           v[2 * i + 1] = kv4_scale<BF16>((uint16_t)(xs[i] >> 16));
         }
-        float back = p.scale_log2;
-        if constexpr (BF16) {
-          float top = 0.f;
+        float top = 0.f;
 #pragma unroll
-          for (int i = 0; i < 8; ++i) top = fmaxf(top, fabsf(v[i]));
-          top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
-          top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
-          int ex = 14 + 127 - (int)(__float_as_uint(top) >> 23);   // top * 2^ex in [2^14, 2^15)
-          ex = ex > 100 ? 100 : ex;
-          const float up = pow2(ex);
-          back = p.scale_log2 * pow2(-ex);
-#pragma unroll
-          for (int i = 0; i < 8; ++i) v[i] *= up;
-        }
+        for (int i = 0; i < 8; ++i) top = fmaxf(top, fabsf(v[i]));
+        top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
+        top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
+        int ex = 14 + 127 - (int)(__float_as_uint(top) >> 23);   // top * 2^ex in [2^14, 2^15)
+        ex = ex > 100 ? 100 : ex;
+        const float up = pow2(ex), back = p.scale_log2 * pow2(-ex);
         float even = 0.f, odd = 0.f;
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-          qb[nt][e][i] = pack2<false>(v[i], v[i + 4]);
+          const float x_up = i & 1 ? up * 0.0625f : up;   // the codes of odd places weigh 16 times those of even ones
+          qb[nt][e][i] = pack2<false>(v[i] * x_up, v[i + 4] * x_up);
           const float2 y = __half22float2(*reinterpret_cast<__half2*>(&qb[nt][e][i]));
           (i & 1 ? odd : even) += y.x + y.y;
         }
-        float c = -(264.f * even + 24.f * odd);
+        float c = -8.f / 16777216.f * back * (even + 16.f * odd);
         c += __shfl_xor_sync(0xffffffffu, c, 1);
         c += __shfl_xor_sync(0xffffffffu, c, 2);
-        init[nt][e][0] = __shfl_sync(0xffffffffu, c, 8 * t);
-        init[nt][e][1] = __shfl_sync(0xffffffffu, c, 8 * t + 4);
+        take[nt][e][0] = __shfl_sync(0xffffffffu, c, 8 * t);
+        take[nt][e][1] = __shfl_sync(0xffffffffu, c, 8 * t + 4);
         f[nt][e][0] = __shfl_sync(0xffffffffu, back, 8 * t);
         f[nt][e][1] = __shfl_sync(0xffffffffu, back, 8 * t + 4);
       }
@@ -343,11 +345,22 @@ __global__ void __launch_bounds__(kThreads, (Shape<D, NT>::CtasPerSm)) fa_kv4_fw
     }
     float v_up = 1.f, v_pass = 0.f;   // s_V goes in times v_up, and may reach v_pass
 
-    for (int s = s0; s < s1; ++s, ++done) {
-      const int slot = (int)(done % ST);
-      alive = warp_all(mbar_wait(bar0 + 8 * slot, (uint32_t)(done / ST) & 1u, wc));
-      if (!alive) break;
-      const uint32_t which = (done / kBatch == (made - 1) / kBatch ? have : have_before) >> (2 * (int)(done % kBatch)) & 3u;
+    for (int s = s0; s < s1; ++s) {
+      const int slot = take_slot;
+      const uint32_t bar = bar0 + 8 * slot;
+      if (!warp_all(mbar_try_wait(bar, phase))) {
+        alive = warp_all(mbar_wait(bar, phase, wc));
+        if (!alive) {
+          flying = (int)(left - to_make - (s - s0));
+          break;
+        }
+      }
+      if (take_at == 0) exist = have;   // the producer is at most ST steps ahead: in the same batch
+      const uint32_t which = exist & 3u;
+      exist >>= 2;
+      take_at = (take_at + 1) % kBatch;
+      take_slot = (take_slot + 1) % ST;
+      phase ^= take_slot == 0;
       const long long key0 = (long long)s * kStep;
       if (which != 0 && key0 < last_key) {
         const uint8_t* const base = ring + slot * 2 * Block;
@@ -380,30 +393,22 @@ __global__ void __launch_bounds__(kThreads, (Shape<D, NT>::CtasPerSm)) fa_kv4_fw
 #pragma unroll
           for (int e = 0; e < W; ++e) {
             const uint32_t x0 = kw[0][e], x1 = kw[1][e];
-            const uint32_t y0 = __byte_perm(x0, 0, 0x2301), y1 = __byte_perm(x1, 0, 0x2301);
-            const uint32_t a0[4] = {(x0 & 0x003c003cu) | 0x5c005c00u, (x1 & 0x003c003cu) | 0x5c005c00u,
-                                    (x0 & 0x03c003c0u) | 0x4c004c00u, (x1 & 0x03c003c0u) | 0x4c004c00u};
-            const uint32_t a1[4] = {(y0 & 0x003c003cu) | 0x5c005c00u, (y1 & 0x003c003cu) | 0x5c005c00u,
-                                    (y0 & 0x03c003c0u) | 0x4c004c00u, (y1 & 0x03c003c0u) | 0x4c004c00u};
+            const uint32_t y0 = x0 >> 8, y1 = x1 >> 8;
+            const uint32_t a0[4] = {x0 & 0x000f000fu, x1 & 0x000f000fu, x0 & 0x00f000f0u, x1 & 0x00f000f0u};
+            const uint32_t a1[4] = {y0 & 0x000f000fu, y1 & 0x000f000fu, y0 & 0x00f000f0u, y1 & 0x00f000f0u};
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt) {
-              const float c[4] = {init[nt][e][0], init[nt][e][1], init[nt][e][0], init[nt][e][1]};
+              const float none[4] = {0.f, 0.f, 0.f, 0.f};
               float d[4];
-              mma16816(d, a0, qb[nt][e][0], qb[nt][e][1], c);
+              mma16816(d, a0, qb[nt][e][0], qb[nt][e][1], none);
               mma16816(d, a1, qb[nt][e][2], qb[nt][e][3], d);
 #pragma unroll
               for (int i = 0; i < 4; ++i) {
-                const float x = BF16 ? d[i] * f[nt][e][i & 1] : d[i];
+                const float x = fmaf(d[i], f[nt][e][i & 1], take[nt][e][i & 1]);
                 sc[nt][bk][i] = e == 0 ? x * sk[i / 2][0] : fmaf(x, sk[i / 2][e], sc[nt][bk][i]);
               }
             }
           }
-        }
-        if constexpr (!BF16) {
-#pragma unroll
-          for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-            for (int i = 0; i < 8; ++i) sc[nt][i / 4][i % 4] *= f[nt][0][i & 1];
         }
         if (which != 3u || key0 + kStep > full_end) {
           // keys that a row does not see; scales behind the last key may be anything
@@ -437,7 +442,7 @@ __global__ void __launch_bounds__(kThreads, (Shape<D, NT>::CtasPerSm)) fa_kv4_fw
         for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
           for (int c = 0; c < 2; ++c) {
-            top[nt][c] = fmaxf(fmax3(sc[nt][0][c], sc[nt][0][2 + c], sc[nt][1][c]), sc[nt][1][2 + c]);
+            top[nt][c] = kUnit * fmaxf(fmax3(sc[nt][0][c], sc[nt][0][2 + c], sc[nt][1][c]), sc[nt][1][2 + c]);
             pass = pass || top[nt][c] > m_pass[nt][c];
           }
         if (__any_sync(0xffffffffu, pass)) {
@@ -479,7 +484,7 @@ __global__ void __launch_bounds__(kThreads, (Shape<D, NT>::CtasPerSm)) fa_kv4_fw
 #pragma unroll
           for (int i = 0; i < 8; ++i) {
             float& x = sc[nt][i / 4][i % 4];
-            x = ex2_approx(x - m[nt][i & 1]);
+            x = ex2_approx(fmaf(x, kUnit, -m[nt][i & 1]));
             l[nt][i & 1] += x;
           }
         // ---- O^T += V^T P^T
@@ -500,15 +505,11 @@ __global__ void __launch_bounds__(kThreads, (Shape<D, NT>::CtasPerSm)) fa_kv4_fw
 #pragma unroll
           for (int e = 0; e < W; ++e) {
             const uint32_t x0 = vw[0][e], x1 = vw[1][e];
-            const uint32_t y0 = __byte_perm(x0, 0, 0x2301), y1 = __byte_perm(x1, 0, 0x2301);
-            const uint32_t a0[4] = {hsub2((x0 & 0x003c003cu) | 0x5c005c00u, 0x5c205c20u),
-                                    hsub2((x0 & 0x03c003c0u) | 0x4c004c00u, 0x4e004e00u),
-                                    hsub2((x1 & 0x003c003cu) | 0x5c005c00u, 0x5c205c20u),
-                                    hsub2((x1 & 0x03c003c0u) | 0x4c004c00u, 0x4e004e00u)};
-            const uint32_t a1[4] = {hsub2((y0 & 0x003c003cu) | 0x5c005c00u, 0x5c205c20u),
-                                    hsub2((y0 & 0x03c003c0u) | 0x4c004c00u, 0x4e004e00u),
-                                    hsub2((y1 & 0x003c003cu) | 0x5c005c00u, 0x5c205c20u),
-                                    hsub2((y1 & 0x03c003c0u) | 0x4c004c00u, 0x4e004e00u)};
+            const uint32_t y0 = x0 >> 8, y1 = x1 >> 8;
+            const uint32_t a0[4] = {hsub2(x0 & 0x000f000fu, 0x00080008u), hsub2(x0 & 0x00f000f0u, 0x00800080u),
+                                    hsub2(x1 & 0x000f000fu, 0x00080008u), hsub2(x1 & 0x00f000f0u, 0x00800080u)};
+            const uint32_t a1[4] = {hsub2(y0 & 0x000f000fu, 0x00080008u), hsub2(y0 & 0x00f000f0u, 0x00800080u),
+                                    hsub2(y1 & 0x000f000fu, 0x00080008u), hsub2(y1 & 0x00f000f0u, 0x00800080u)};
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt) {
               const float(&pr)[4] = sc[nt][bk];
@@ -521,7 +522,7 @@ __global__ void __launch_bounds__(kThreads, (Shape<D, NT>::CtasPerSm)) fa_kv4_fw
         }
       }
       __syncwarp();
-      if (made < todo) produce();
+      if (to_make > 0) produce();
     }
     if (!alive) break;
 
@@ -537,11 +538,11 @@ __global__ void __launch_bounds__(kThreads, (Shape<D, NT>::CtasPerSm)) fa_kv4_fw
         float ll = quad_sum(l[nt][c]), mm = m_pass[nt][c] == -INFINITY ? -INFINITY : m[nt][c];
         if (row >= rows) continue;
         if (lim[nt][c] == 0) ll = 0.f, mm = -INFINITY;   // steps that all other rows see whole do not mask this one
-        const float inv = ll == 0.f ? 0.f : 1.f / ll;
+        const float even = ll == 0.f ? 0.f : kUnit / ll, odd = even * 0.0625f;
 #pragma unroll
         for (int e = 0; e < W; ++e) {
-          const float4 x = make_float4(o[nt][e][0][c] * inv * v_down, o[nt][e][0][2 + c] * inv * v_down,
-                                       o[nt][e][1][c] * inv * v_down, o[nt][e][1][2 + c] * inv * v_down);
+          const float4 x = make_float4(o[nt][e][0][c] * even * v_down, o[nt][e][0][2 + c] * odd * v_down,
+                                       o[nt][e][1][c] * even * v_down, o[nt][e][1][2 + c] * odd * v_down);
           const int col = 32 * e + 4 * g;
           if (part != nullptr)
             *reinterpret_cast<float4*>(part + row * D + col) = x;
@@ -564,12 +565,16 @@ __global__ void __launch_bounds__(kThreads, (Shape<D, NT>::CtasPerSm)) fa_kv4_fw
       join.parts = (int)((r.steps - s1 + each - 1) / each);
     }
     at.rem += s1 - s0;
+    left -= s1 - s0;
     at.settle(p);
   }
   if (!alive) {
     // copies in flight land before the CTA's shared memory goes
-    for (; done < made; ++done)
-      if (!warp_all(mbar_wait_drain(bar0 + 8 * (int)(done % ST), (uint32_t)(done / ST) & 1u, p.wait_limit_ns))) break;
+    for (; flying > 0; --flying) {
+      mbar_wait_drain(bar0 + 8 * take_slot, phase, p.wait_limit_ns);
+      take_slot = (take_slot + 1) % ST;
+      phase ^= take_slot == 0;
+    }
     join.parts = 0;
   }
   if (lane == 0) p.joins[worker] = join;
