@@ -57,11 +57,11 @@ constexpr float kLazy = 8.f;            // log2 by which a score may pass the ru
 
 template <int D, int NT>
 struct Shape {
-  static constexpr int W = D / 32, Rows = 8 * NT, Block = kv4_block_bytes(D), Stages = 4;
+  static constexpr int W = D / 32, Rows = 8 * NT, Block = kv4_block_bytes(D), Stages = 2;
   // registers a thread allow this many CTAs a SM
   static constexpr int CtasPerSm = W * NT <= 4 ? 3 : 2;
   static constexpr int Slot = Rows * (D + 2);   // floats of a partial result: O, then m and l by row
-  static constexpr size_t Smem = (size_t)kWarps * Stages * 2 * Block;
+  static constexpr size_t Smem = (size_t)kWarps * Stages * 4 * Block;
 };
 
 __device__ __forceinline__ void mma16816(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1,
@@ -146,10 +146,10 @@ __global__ void __launch_bounds__(kThreads, (Shape<D, NT>::CtasPerSm)) fa_kv4_fw
   __shared__ int abort_flag;
 
   const int lane = threadIdx.x % 32, warp = threadIdx.x / 32, g = lane / 4, t = lane % 4;
-  uint8_t* const ring = ring_all + (size_t)warp * ST * 2 * Block;
+  uint8_t* const ring = ring_all + (size_t)warp * ST * 4 * Block;
   const uint32_t bar0 = smem_u32(&bars[warp][0]), ring0 = smem_u32(ring);
   if (threadIdx.x == 0) abort_flag = 0;
-  if (lane < ST) mbar_init(bar0 + 8 * lane, 2);
+  if (lane < ST) mbar_init(bar0 + 8 * lane, 4);
   fence_mbar_init();
   grid_dependency_wait();
   grid_dependents_launch();
@@ -225,7 +225,7 @@ __global__ void __launch_bounds__(kThreads, (Shape<D, NT>::CtasPerSm)) fa_kv4_fw
   const uint8_t* src = nullptr;
   uint32_t have = 0;              // which blocks of this batch exist
   long long to_make = todo;
-  int make_at = 0, make_slot = 0;   // the step's place in its batch and in the ring
+  int make_at = 0, make_slot = 0;   // the pair of steps' place in its batch and in the ring
   auto produce = [&]() {
     if (make_at == 0) {
       const bool ok = page_next >= 0 && page_next < p.c.n_pages;
@@ -234,18 +234,18 @@ __global__ void __launch_bounds__(kThreads, (Shape<D, NT>::CtasPerSm)) fa_kv4_fw
       have = __ballot_sync(0xffffffffu, ok);
       look_up();
     }
-    if (lane / 2 == make_at) {
+    if (lane / 4 == make_at) {
       const uint32_t bar = bar0 + 8 * make_slot;
       if (src != nullptr) {
         mbar_arrive_expect_tx(bar, Block);
-        bulk_load(ring0 + (make_slot * 2 + (lane & 1)) * Block, src, Block, bar);
+        bulk_load(ring0 + (make_slot * 4 + lane % 4) * Block, src, Block, bar);
       } else {
         mbar_arrive(bar);
       }
     }
-    make_at = (make_at + 1) % kBatch;
-    make_slot = (make_slot + 1) % ST;
-    --to_make;
+    make_at = (make_at + 1) % (kBatch / 2);
+    make_slot ^= 1;
+    to_make -= 2;
   };
   look_up();
 #pragma unroll
@@ -258,10 +258,10 @@ __global__ void __launch_bounds__(kThreads, (Shape<D, NT>::CtasPerSm)) fa_kv4_fw
   const long long unit_rows = (long long)group * p.T;
   long long left = todo;
   uint32_t exist = 0;                          // as `have`, from the step to come on
-  int take_at = 0, take_slot = 0;              // as make_at and make_slot
+  int take = 0;                                // the step's place in its batch
   uint32_t phase = 0;
   bool alive = true;
-  int flying = 0;                              // steps on their way when a wait ran out
+  int flying = 0;                              // pairs of steps on their way when a wait ran out
 
   while (left > 0 && alive) {
     // ---- one unit's share
@@ -275,7 +275,7 @@ __global__ void __launch_bounds__(kThreads, (Shape<D, NT>::CtasPerSm)) fa_kv4_fw
     const int rows = unit_rows - row_in < Sh::Rows ? (int)(unit_rows - row_in) : Sh::Rows;
 
     uint32_t qb[NT][W][4];
-    float take[NT][W][2], f[NT][W][2];   // of the rows of this lane's columns
+    float fix[NT][W][2], f[NT][W][2];   // of the rows of this lane's columns
     int lim[NT][2];
     int full_end = 0x7fffffff, last_key = 0;
     const long long cap = (long long)p.c.max_pages << p.c.page_shift;
@@ -320,8 +320,8 @@ __global__ void __launch_bounds__(kThreads, (Shape<D, NT>::CtasPerSm)) fa_kv4_fw
         float c = -8.f / 16777216.f * back * (even + 16.f * odd);
         c += __shfl_xor_sync(0xffffffffu, c, 1);
         c += __shfl_xor_sync(0xffffffffu, c, 2);
-        take[nt][e][0] = __shfl_sync(0xffffffffu, c, 8 * t);
-        take[nt][e][1] = __shfl_sync(0xffffffffu, c, 8 * t + 4);
+        fix[nt][e][0] = __shfl_sync(0xffffffffu, c, 8 * t);
+        fix[nt][e][1] = __shfl_sync(0xffffffffu, c, 8 * t + 4);
         f[nt][e][0] = __shfl_sync(0xffffffffu, back, 8 * t);
         f[nt][e][1] = __shfl_sync(0xffffffffu, back, 8 * t + 4);
       }
@@ -346,24 +346,23 @@ __global__ void __launch_bounds__(kThreads, (Shape<D, NT>::CtasPerSm)) fa_kv4_fw
     float v_up = 1.f, v_pass = 0.f;   // s_V goes in times v_up, and may reach v_pass
 
     for (int s = s0; s < s1; ++s) {
-      const int slot = take_slot;
-      const uint32_t bar = bar0 + 8 * slot;
-      if (!warp_all(mbar_try_wait(bar, phase))) {
-        alive = warp_all(mbar_wait(bar, phase, wc));
-        if (!alive) {
-          flying = (int)(left - to_make - (s - s0));
-          break;
+      const int slot = take / 2 % ST;
+      if (take % 2 == 0) {
+        const uint32_t bar = bar0 + 8 * slot;
+        if (!warp_all(mbar_try_wait(bar, phase))) {
+          alive = warp_all(mbar_wait(bar, phase, wc));
+          if (!alive) {
+            flying = (int)((left - (s - s0) + 1) / 2 - (to_make > 0 ? (to_make + 1) / 2 : 0));
+            break;
+          }
         }
+        if (take == 0) exist = have;   // the producer is at most ST pairs ahead: in the same batch
       }
-      if (take_at == 0) exist = have;   // the producer is at most ST steps ahead: in the same batch
       const uint32_t which = exist & 3u;
       exist >>= 2;
-      take_at = (take_at + 1) % kBatch;
-      take_slot = (take_slot + 1) % ST;
-      phase ^= take_slot == 0;
       const long long key0 = (long long)s * kStep;
       if (which != 0 && key0 < last_key) {
-        const uint8_t* const base = ring + slot * 2 * Block;
+        const uint8_t* const base = ring + (slot * 2 + take % 2) * 2 * Block;
         float sc[NT][2][4], sv[2][2][W];
 #pragma unroll
         for (int bk = 0; bk < 2; ++bk) {
@@ -403,9 +402,13 @@ __global__ void __launch_bounds__(kThreads, (Shape<D, NT>::CtasPerSm)) fa_kv4_fw
               mma16816(d, a0, qb[nt][e][0], qb[nt][e][1], none);
               mma16816(d, a1, qb[nt][e][2], qb[nt][e][3], d);
 #pragma unroll
-              for (int i = 0; i < 4; ++i) {
-                const float x = fmaf(d[i], f[nt][e][i & 1], take[nt][e][i & 1]);
-                sc[nt][bk][i] = e == 0 ? x * sk[i / 2][0] : fmaf(x, sk[i / 2][e], sc[nt][bk][i]);
+              for (int half = 0; half < 2; ++half) {
+                float x0, x1;
+                f2_unpack(f2_fma(f2_pack(d[2 * half], d[2 * half + 1]), f2_pack(f[nt][e][0], f[nt][e][1]),
+                                 f2_pack(fix[nt][e][0], fix[nt][e][1])), x0, x1);
+                float(&out)[4] = sc[nt][bk];
+                out[2 * half] = e == 0 ? x0 * sk[half][0] : fmaf(x0, sk[half][e], out[2 * half]);
+                out[2 * half + 1] = e == 0 ? x1 * sk[half][0] : fmaf(x1, sk[half][e], out[2 * half + 1]);
               }
             }
           }
@@ -452,7 +455,7 @@ __global__ void __launch_bounds__(kThreads, (Shape<D, NT>::CtasPerSm)) fa_kv4_fw
           float fv = 1.f;
           if (all > v_pass) {
             int ex = (int)(__float_as_uint(all) >> 23) - 127;
-            ex = ex < -114 ? -114 : ex;
+            ex = ex < -106 ? -106 : ex;   // P v_up stays finite
             const float up = pow2(6 - ex);
             fv = v_pass == 0.f ? 0.f : up / v_up;   // nothing to scale before the first value
             v_up = up;
@@ -478,15 +481,20 @@ __global__ void __launch_bounds__(kThreads, (Shape<D, NT>::CtasPerSm)) fa_kv4_fw
             }
         }
 #pragma unroll
-        for (int i = 0; i < 4 * W; ++i) sv[i / (2 * W)][i / W % 2][i % W] *= v_up;
+        for (int nt = 0; nt < NT; ++nt) {
+          uint64_t sum = f2_pack(l[nt][0], l[nt][1]);
+          const uint64_t neg = f2_pack(-m[nt][0], -m[nt][1]);
 #pragma unroll
-        for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-          for (int i = 0; i < 8; ++i) {
-            float& x = sc[nt][i / 4][i % 4];
-            x = ex2_approx(fmaf(x, kUnit, -m[nt][i & 1]));
-            l[nt][i & 1] += x;
+          for (int i = 0; i < 4; ++i) {
+            float(&x)[4] = sc[nt][i / 2];
+            float x0, x1;
+            f2_unpack(f2_fma(f2_pack(x[2 * (i % 2)], x[2 * (i % 2) + 1]), f2_pack(kUnit, kUnit), neg), x0, x1);
+            const uint64_t pp = f2_pack(ex2_approx(x0), ex2_approx(x1));
+            sum = f2_add(sum, pp);
+            f2_unpack(f2_mul(pp, f2_pack(v_up, v_up)), x[2 * (i % 2)], x[2 * (i % 2) + 1]);
           }
+          f2_unpack(sum, l[nt][0], l[nt][1]);
+        }
         // ---- O^T += V^T P^T
 #pragma unroll
         for (int bk = 0; bk < 2; ++bk) {
@@ -521,8 +529,12 @@ __global__ void __launch_bounds__(kThreads, (Shape<D, NT>::CtasPerSm)) fa_kv4_fw
           }
         }
       }
-      __syncwarp();
-      if (to_make > 0) produce();
+      if (take % 2 != 0) {
+        __syncwarp();
+        if (to_make > 0) produce();
+        phase ^= slot == ST - 1;
+      }
+      take = (take + 1) % kBatch;
     }
     if (!alive) break;
 
@@ -571,9 +583,10 @@ __global__ void __launch_bounds__(kThreads, (Shape<D, NT>::CtasPerSm)) fa_kv4_fw
   if (!alive) {
     // copies in flight land before the CTA's shared memory goes
     for (; flying > 0; --flying) {
-      mbar_wait_drain(bar0 + 8 * take_slot, phase, p.wait_limit_ns);
-      take_slot = (take_slot + 1) % ST;
-      phase ^= take_slot == 0;
+      const int slot = take / 2 % ST;
+      mbar_wait_drain(bar0 + 8 * slot, phase, p.wait_limit_ns);
+      phase ^= slot == ST - 1;
+      take = (take + 2) % kBatch;
     }
     join.parts = 0;
   }
