@@ -59,9 +59,10 @@ template <int D, int NT>
 struct Shape {
   static constexpr int W = D / 32, Rows = 8 * NT, Block = kv4_block_bytes(D), Stages = 2;
   // registers a thread allow this many CTAs a SM
-  static constexpr int CtasPerSm = W * NT <= 4 ? 3 : 2;
+  static constexpr int CtasPerSm = W * NT <= 2 ? 4 : W * NT <= 4 ? 3 : 2;
   static constexpr int Slot = Rows * (D + 2);   // floats of a partial result: O, then m and l by row
-  static constexpr size_t Smem = (size_t)kWarps * Stages * 4 * Block;
+  static constexpr int RowBytes = 4 * NT * W * 16;   // per warp: each column pair's factors and offsets
+  static constexpr size_t Smem = (size_t)kWarps * (Stages * 4 * Block + RowBytes);
 };
 
 __device__ __forceinline__ void mma16816(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1,
@@ -69,6 +70,17 @@ __device__ __forceinline__ void mma16816(float (&d)[4], const uint32_t (&a)[4], 
   asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%10,%11,%12,%13};"
       : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
       : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1), "f"(c[0]), "f"(c[1]), "f"(c[2]), "f"(c[3]));
+}
+
+// Of both half-words, the one of larger magnitude (its sign is of no use).
+template <bool BF16>
+__device__ __forceinline__ uint32_t max_abs2(uint32_t a, uint32_t b) {
+  uint32_t r;
+  if constexpr (BF16)
+    asm("max.xorsign.abs.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+  else
+    asm("max.xorsign.abs.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+  return r;
 }
 
 __device__ __forceinline__ uint32_t transpose8x8(uint32_t x) {
@@ -147,6 +159,7 @@ __global__ void __launch_bounds__(kThreads, (Shape<D, NT>::CtasPerSm)) fa_kv4_fw
 
   const int lane = threadIdx.x % 32, warp = threadIdx.x / 32, g = lane / 4, t = lane % 4;
   uint8_t* const ring = ring_all + (size_t)warp * ST * 4 * Block;
+  float4* const fix = reinterpret_cast<float4*>(ring_all + (size_t)kWarps * ST * 4 * Block + warp * Sh::RowBytes) + t;
   const uint32_t bar0 = smem_u32(&bars[warp][0]), ring0 = smem_u32(ring);
   if (threadIdx.x == 0) abort_flag = 0;
   if (lane < ST) mbar_init(bar0 + 8 * lane, 4);
@@ -275,7 +288,6 @@ __global__ void __launch_bounds__(kThreads, (Shape<D, NT>::CtasPerSm)) fa_kv4_fw
     const int rows = unit_rows - row_in < Sh::Rows ? (int)(unit_rows - row_in) : Sh::Rows;
 
     uint32_t qb[NT][W][4];
-    float fix[NT][W][2], f[NT][W][2];   // of the rows of this lane's columns
     int lim[NT][2];
     int full_end = 0x7fffffff, last_key = 0;
     const long long cap = (long long)p.c.max_pages << p.c.page_shift;
@@ -320,16 +332,17 @@ __global__ void __launch_bounds__(kThreads, (Shape<D, NT>::CtasPerSm)) fa_kv4_fw
         float c = -8.f / 16777216.f * back * (even + 16.f * odd);
         c += __shfl_xor_sync(0xffffffffu, c, 1);
         c += __shfl_xor_sync(0xffffffffu, c, 2);
-        fix[nt][e][0] = __shfl_sync(0xffffffffu, c, 8 * t);
-        fix[nt][e][1] = __shfl_sync(0xffffffffu, c, 8 * t + 4);
-        f[nt][e][0] = __shfl_sync(0xffffffffu, back, 8 * t);
-        f[nt][e][1] = __shfl_sync(0xffffffffu, back, 8 * t + 4);
+        const float4 both = make_float4(__shfl_sync(0xffffffffu, back, 8 * t), __shfl_sync(0xffffffffu, back, 8 * t + 4),
+                                        __shfl_sync(0xffffffffu, c, 8 * t), __shfl_sync(0xffffffffu, c, 8 * t + 4));
+        __syncwarp();
+        fix[4 * (nt * W + e)] = both;   // all lanes of a column pair write the same
       }
       if (my_lim > 0) full_end = min(full_end, my_lim);
       last_key = max(last_key, my_lim);
       lim[nt][0] = __shfl_sync(0xffffffffu, my_lim, 8 * t);
       lim[nt][1] = __shfl_sync(0xffffffffu, my_lim, 8 * t + 4);
     }
+    __syncwarp();
     full_end = __reduce_min_sync(0xffffffffu, full_end);
     last_key = __reduce_max_sync(0xffffffffu, last_key);
 
@@ -363,7 +376,8 @@ __global__ void __launch_bounds__(kThreads, (Shape<D, NT>::CtasPerSm)) fa_kv4_fw
       const long long key0 = (long long)s * kStep;
       if (which != 0 && key0 < last_key) {
         const uint8_t* const base = ring + (slot * 2 + take % 2) * 2 * Block;
-        float sc[NT][2][4], sv[2][2][W];
+        float sc[NT][2][4];
+        uint32_t vs[2][2][W / 2];   // V's scales, two to a word
 #pragma unroll
         for (int bk = 0; bk < 2; ++bk) {
           const uint8_t* blk = base + bk * Block;
@@ -386,8 +400,9 @@ __global__ void __launch_bounds__(kThreads, (Shape<D, NT>::CtasPerSm)) fa_kv4_fw
 #pragma unroll
             for (int e = 0; e < W; ++e) {
               sk[half][e] = kv4_scale<BF16>((uint16_t)(raw[e / 2] >> (16 * (e & 1))));
-              sv[bk][half][e] = kv4_scale<BF16>((uint16_t)(raw[W / 2 + e / 2] >> (16 * (e & 1))));
             }
+#pragma unroll
+            for (int e = 0; e < W / 2; ++e) vs[bk][half][e] = raw[W / 2 + e];
           }
 #pragma unroll
           for (int e = 0; e < W; ++e) {
@@ -397,6 +412,7 @@ __global__ void __launch_bounds__(kThreads, (Shape<D, NT>::CtasPerSm)) fa_kv4_fw
             const uint32_t a1[4] = {y0 & 0x000f000fu, y1 & 0x000f000fu, y0 & 0x00f000f0u, y1 & 0x00f000f0u};
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt) {
+              const float4 fx = fix[4 * (nt * W + e)];
               const float none[4] = {0.f, 0.f, 0.f, 0.f};
               float d[4];
               mma16816(d, a0, qb[nt][e][0], qb[nt][e][1], none);
@@ -404,8 +420,7 @@ __global__ void __launch_bounds__(kThreads, (Shape<D, NT>::CtasPerSm)) fa_kv4_fw
 #pragma unroll
               for (int half = 0; half < 2; ++half) {
                 float x0, x1;
-                f2_unpack(f2_fma(f2_pack(d[2 * half], d[2 * half + 1]), f2_pack(f[nt][e][0], f[nt][e][1]),
-                                 f2_pack(fix[nt][e][0], fix[nt][e][1])), x0, x1);
+                f2_unpack(f2_fma(f2_pack(d[2 * half], d[2 * half + 1]), f2_pack(fx.x, fx.y), f2_pack(fx.z, fx.w)), x0, x1);
                 float(&out)[4] = sc[nt][bk];
                 out[2 * half] = e == 0 ? x0 * sk[half][0] : fmaf(x0, sk[half][e], out[2 * half]);
                 out[2 * half + 1] = e == 0 ? x1 * sk[half][0] : fmaf(x1, sk[half][e], out[2 * half + 1]);
@@ -423,7 +438,7 @@ __global__ void __launch_bounds__(kThreads, (Shape<D, NT>::CtasPerSm)) fa_kv4_fw
               const bool there = (which >> bk & 1u) != 0;
               if (!there || key >= last_key) {
 #pragma unroll
-                for (int e = 0; e < W; ++e) sv[bk][half][e] = 0.f;
+                for (int e = 0; e < W / 2; ++e) vs[bk][half][e] = 0;
               }
 #pragma unroll
               for (int nt = 0; nt < NT; ++nt)
@@ -433,12 +448,12 @@ __global__ void __launch_bounds__(kThreads, (Shape<D, NT>::CtasPerSm)) fa_kv4_fw
             }
         }
         // ---- V's scales, relative to the largest so far
-        float v_top = 0.f;
+        uint32_t top2 = 0;
 #pragma unroll
         for (int i = 0; i < 4; ++i)
 #pragma unroll
-          for (int e = 0; e < W; e += 2)
-            v_top = fmax3(v_top, fabsf(sv[i / 2][i % 2][e]), fabsf(sv[i / 2][i % 2][e + 1]));
+          for (int e = 0; e < W / 2; ++e) top2 = max_abs2<BF16>(top2, vs[i / 2][i % 2][e]);
+        const float v_top = fmaxf(fabsf(kv4_scale<BF16>((uint16_t)top2)), fabsf(kv4_scale<BF16>((uint16_t)(top2 >> 16))));
         bool pass = v_top > v_pass;
         float top[NT][2];
 #pragma unroll
@@ -518,11 +533,13 @@ __global__ void __launch_bounds__(kThreads, (Shape<D, NT>::CtasPerSm)) fa_kv4_fw
                                     hsub2(x1 & 0x000f000fu, 0x00080008u), hsub2(x1 & 0x00f000f0u, 0x00800080u)};
             const uint32_t a1[4] = {hsub2(y0 & 0x000f000fu, 0x00080008u), hsub2(y0 & 0x00f000f0u, 0x00800080u),
                                     hsub2(y1 & 0x000f000fu, 0x00080008u), hsub2(y1 & 0x00f000f0u, 0x00800080u)};
+            const float s0 = kv4_scale<BF16>((uint16_t)(vs[bk][0][e / 2] >> (16 * (e & 1))));
+            const float s1 = kv4_scale<BF16>((uint16_t)(vs[bk][1][e / 2] >> (16 * (e & 1))));
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt) {
               const float(&pr)[4] = sc[nt][bk];
-              const uint32_t b0 = transpose8x8(pack2<false>(pr[0] * sv[bk][0][e], pr[1] * sv[bk][0][e]));
-              const uint32_t b1 = transpose8x8(pack2<false>(pr[2] * sv[bk][1][e], pr[3] * sv[bk][1][e]));
+              const uint32_t b0 = transpose8x8(pack2<false>(pr[0] * s0, pr[1] * s0));
+              const uint32_t b1 = transpose8x8(pack2<false>(pr[2] * s1, pr[3] * s1));
               mma16816(o[nt][e][0], a0, b0, b1, o[nt][e][0]);
               mma16816(o[nt][e][1], a1, b0, b1, o[nt][e][1]);
             }
@@ -596,41 +613,78 @@ __global__ void __launch_bounds__(kThreads, (Shape<D, NT>::CtasPerSm)) fa_kv4_fw
 // O and LSE of the units that lie across workers: one CTA for each worker in
 // which such a unit begins.  Pieces are normalised, with their maximum m (in
 // log2) and sum l beside them; a piece that saw no key has m = -inf, l = 0.
+// Four elements of a row to a thread; threads to spare take the pieces in
+// turn, eight at a time in flight.
+constexpr int kJoinThreads = 512;
+
+struct Piece {
+  float4 o;
+  float m, l;
+
+  // The two as one; o stays a sum weighted by l.
+  __device__ __forceinline__ void add(const float4& x, float xm, float xl) {
+    const float top = fmaxf(m, xm);
+    const float fa = m == -INFINITY ? 1.f : ex2_approx(m - top);   // o and l are 0 or NaN while m is -inf
+    const float fb = xm == -INFINITY ? 1.f : ex2_approx(xm - top);
+    o.x = o.x * fa + x.x * fb, o.y = o.y * fa + x.y * fb;
+    o.z = o.z * fa + x.z * fb, o.w = o.w * fa + x.w * fb;
+    l = l * fa + xl * fb;
+    m = top;
+  }
+};
+
 template <bool BF16, int D, int NT>
-__global__ void __launch_bounds__(256) fa_kv4_join_kernel(const Kv4FwdParams p) {
+__global__ void __launch_bounds__(kJoinThreads) fa_kv4_join_kernel(const Kv4FwdParams p) {
   using Sh = Shape<D, NT>;
+  static_assert(Sh::Rows * D / 4 <= kJoinThreads, "a thread holds four elements");
+  __shared__ Piece shared[kJoinThreads];
   grid_dependency_wait();
   grid_dependents_launch();
   const long long worker = blockIdx.x;
   const Kv4Join j = p.joins[worker];
   if (j.parts == 0) return;
-  for (int i = threadIdx.x; i < j.rows * (D / 4); i += 256) {
-    const int row = i / (D / 4), col = 4 * (i % (D / 4));
-    float mm = -INFINITY, ll = 0.f;
-    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 4
-    for (int k = 0; k <= j.parts; ++k) {
-      const float* part = slot_of(p, worker + k, k == 0 ? 1 : 0, Sh::Slot);
-      const float2 ml = *reinterpret_cast<const float2*>(part + Sh::Rows * D + 2 * row);
-      const float4 x = *reinterpret_cast<const float4*>(part + row * D + col);
-      const float mn = fmaxf(mm, ml.x);
-      const float fa = mm == -INFINITY ? 1.f : ex2_approx(mm - mn);             // ll and acc are 0 or NaN while mm is -inf
-      const float fb = ml.x == -INFINITY ? ml.y : ml.y * ex2_approx(ml.x - mn);
-      ll = ll * fa + fb;
-      acc.x = acc.x * fa + x.x * fb, acc.y = acc.y * fa + x.y * fb;
-      acc.z = acc.z * fa + x.z * fb, acc.w = acc.w * fa + x.w * fb;
-      mm = mn;
+  const int items = j.rows * (D / 4), turns = min(kJoinThreads / items, j.parts + 1);
+  const int item = threadIdx.x % items, turn = threadIdx.x / items, row = item / (D / 4), col = 4 * (item % (D / 4));
+  Piece mine{make_float4(0.f, 0.f, 0.f, 0.f), -INFINITY, 0.f};
+  if (turn < turns) {
+    constexpr int kFly = 8;
+    for (int k0 = turn; k0 <= j.parts; k0 += kFly * turns) {
+      float4 x[kFly];
+      float2 ml[kFly];
+#pragma unroll
+      for (int i = 0; i < kFly; ++i) {
+        const int k = k0 + i * turns;
+        ml[i] = make_float2(-INFINITY, 0.f);
+        x[i] = make_float4(0.f, 0.f, 0.f, 0.f);
+        if (k <= j.parts) {
+          const float* part = slot_of(p, worker + k, k == 0 ? 1 : 0, Sh::Slot);
+          ml[i] = *reinterpret_cast<const float2*>(part + Sh::Rows * D + 2 * row);
+          x[i] = *reinterpret_cast<const float4*>(part + row * D + col);
+        }
+      }
+#pragma unroll
+      for (int i = 0; i < kFly; ++i) {
+        const float l = ml[i].y;
+        mine.add(make_float4(x[i].x * l, x[i].y * l, x[i].z * l, x[i].w * l), ml[i].x, l);
+      }
     }
-    const float inv = ll == 0.f ? 0.f : 1.f / ll;
-    acc.x *= inv, acc.y *= inv, acc.z *= inv, acc.w *= inv;
-    const long long at = (j.row + row) * D + col;
-    if (p.o32)
-      *reinterpret_cast<float4*>(static_cast<float*>(p.o) + at) = acc;
-    else
-      *reinterpret_cast<uint2*>(static_cast<uint16_t*>(p.o) + at) =
-          make_uint2(pack2<BF16>(acc.x, acc.y), pack2<BF16>(acc.z, acc.w));
-    if (col == 0) p.lse[j.row + row] = (mm + log2f(ll)) * 0.69314718055994531f;
+    shared[threadIdx.x] = mine;
   }
+  __syncthreads();
+  if (turn != 0) return;
+  for (int k = 1; k < turns; ++k) {
+    const Piece& x = shared[k * items + item];
+    mine.add(x.o, x.m, x.l);
+  }
+  const float inv = mine.l == 0.f ? 0.f : 1.f / mine.l;
+  const float4 acc = make_float4(mine.o.x * inv, mine.o.y * inv, mine.o.z * inv, mine.o.w * inv);
+  const long long at = (j.row + row) * D + col;
+  if (p.o32)
+    *reinterpret_cast<float4*>(static_cast<float*>(p.o) + at) = acc;
+  else
+    *reinterpret_cast<uint2*>(static_cast<uint16_t*>(p.o) + at) =
+        make_uint2(pack2<BF16>(acc.x, acc.y), pack2<BF16>(acc.z, acc.w));
+  if (col == 0) p.lse[j.row + row] = (mine.m + log2f(mine.l)) * 0.69314718055994531f;
 }
 
 constexpr int kMaxSms = 160;
@@ -646,19 +700,19 @@ cudaError_t launch(Kv4FwdParams p, void* workspace, int sms, cudaStream_t st) {
   p.units_per_seq = (long long)p.c.Hkv * p.row_tiles;
   const int grid = (sms < kMaxSms ? sms : kMaxSms) * Sh::CtasPerSm;
   p.joins = static_cast<Kv4Join*>(workspace);
-  p.partials = reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + sizeof(Kv4Join) * kMaxSms * kWarps * 3);
+  p.partials = reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + sizeof(Kv4Join) * kMaxSms * kWarps * 4);
   auto kern = fa_kv4_fwd_kernel<BF16, D, NT>;
   cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)Sh::Smem);
   if (e != cudaSuccess) return e;
   if ((e = launch_chained(kern, dim3(grid), dim3(kThreads), Sh::Smem, st, p)) != cudaSuccess) return e;
-  return launch_chained(fa_kv4_join_kernel<BF16, D, NT>, dim3(grid * kWarps), dim3(256), 0, st, p);
+  return launch_chained(fa_kv4_join_kernel<BF16, D, NT>, dim3(grid * kWarps), dim3(kJoinThreads), 0, st, p);
 }
 
 }  // namespace
 
 size_t kv4_fwd_workspace(int d, long long rows) {
-  const int nt = row_tiles_of(d, rows), ctas = d / 32 * nt <= 4 ? 3 : 2;
-  return sizeof(Kv4Join) * kMaxSms * kWarps * 3 + (size_t)kMaxSms * ctas * kWarps * 2 * (8 * nt) * (d + 2) * 4;
+  const int nt = row_tiles_of(d, rows), ctas = d / 32 * nt <= 2 ? 4 : d / 32 * nt <= 4 ? 3 : 2;
+  return sizeof(Kv4Join) * kMaxSms * kWarps * 4 + (size_t)kMaxSms * ctas * kWarps * 2 * (8 * nt) * (d + 2) * 4;
 }
 
 cudaError_t launch_kv4_fwd(bool bf16, int d, const Kv4FwdParams& p, void* workspace, int sms, cudaStream_t st) {
