@@ -53,16 +53,22 @@ constexpr int kStep = 32;               // keys of a step: two blocks
 constexpr int kBatch = 16;              // steps whose pages a warp looks up at once
 constexpr int kMinSteps = 2;            // least steps worth a warp
 constexpr float kUnit = 16777216.f;     // scores and O are summed in units of 2^-24, the subnormals' step
+constexpr float kLeast = -3.402823466e38f;   // a maximum before the first key
+constexpr float kVPass = 128.f;              // with P below 2^8, P s_V stays in fp16's range
+constexpr int kMostUp = 106;                 // P v_up stays finite
 constexpr float kLazy = 8.f;            // log2 by which a score may pass the running maximum
 
 template <int D, int NT>
 struct Shape {
-  static constexpr int W = D / 32, Rows = 8 * NT, Block = kv4_block_bytes(D), Stages = 2;
-  // registers a thread allow this many CTAs a SM
+  static constexpr int W = D / 32, Rows = 8 * NT, Block = kv4_block_bytes(D);
+  // CTAs a SM, as registers allow, and how its shared memory is cut into
+  // stages: of Per steps each, Stages to a warp.
   static constexpr int CtasPerSm = W * NT <= 2 ? 4 : W * NT <= 4 ? 3 : 2;
+  static constexpr int Per = CtasPerSm == 4 && D == 128 ? 1 : 2, Stages = Per == 1 ? 3 : 2;
   static constexpr int Slot = Rows * (D + 2);   // floats of a partial result: O, then m and l by row
   static constexpr int RowBytes = 4 * NT * W * 16;   // per warp: each column pair's factors and offsets
-  static constexpr size_t Smem = (size_t)kWarps * (Stages * 4 * Block + RowBytes);
+  static constexpr int Stage = Per * 2 * Block;
+  static constexpr size_t Smem = (size_t)kWarps * (Stages * Stage + RowBytes);
 };
 
 __device__ __forceinline__ void mma16816(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1,
@@ -81,6 +87,22 @@ __device__ __forceinline__ uint32_t max_abs2(uint32_t a, uint32_t b) {
   else
     asm("max.xorsign.abs.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
   return r;
+}
+
+// The scale in the low or high half of a word; a mixed-precision addition, as
+// the integer pipe is the busier one.
+template <bool BF16>
+__device__ __forceinline__ float scale_half(uint32_t w, int high) {
+  if constexpr (BF16) {
+    float r;
+    if (high)
+      asm("{.reg .b16 l, h; mov.b32 {l, h}, %1; add.f32.bf16 %0, h, %2;}" : "=f"(r) : "r"(w), "f"(-0.f));
+    else
+      asm("{.reg .b16 l, h; mov.b32 {l, h}, %1; add.f32.bf16 %0, l, %2;}" : "=f"(r) : "r"(w), "f"(-0.f));
+    return r;
+  } else {
+    return kv4_scale<false>((uint16_t)(w >> (16 * high)));
+  }
 }
 
 __device__ __forceinline__ uint32_t transpose8x8(uint32_t x) {
@@ -130,19 +152,29 @@ __device__ __forceinline__ Reach reach(const Kv4FwdParams& p, int b) {
   return r;
 }
 
-// A position in the sequence of all steps.
+// A position in the sequence of all steps: `rem` steps behind the first one of
+// sequence b.  settle moves it on to the sequence that it lies in and returns
+// how far that one reaches.
 struct Cursor {
   int b;
-  long long rem;   // steps behind the first of sequence b
-  Reach r;
+  long long rem;
 
-  __device__ __forceinline__ void settle(const Kv4FwdParams& p) {
-    while (b < p.B && rem >= (long long)r.steps * p.units_per_seq) {
+  __device__ __forceinline__ Reach settle(const Kv4FwdParams& p) {
+    Reach r = reach(p, b);
+    while (rem >= (long long)r.steps * p.units_per_seq) {
+      if (b == p.B - 1) break;   // behind the last step
       rem -= (long long)r.steps * p.units_per_seq;
-      if (++b < p.B) r = reach(p, b);
+      r = reach(p, ++b);
     }
+    return r;
   }
 };
+
+// Which of the sequence's units a position lies in.
+__device__ __forceinline__ unsigned unit_at(long long rem, int steps) {
+  if (rem >> 32 == 0) return (unsigned)rem / (unsigned)steps;
+  return (unsigned)((unsigned long long)rem / (unsigned)steps);
+}
 
 __device__ __forceinline__ float* slot_of(const Kv4FwdParams& p, long long worker, int which, int slot_floats) {
   return p.partials + (size_t)(2 * worker + which) * slot_floats;
@@ -151,18 +183,19 @@ __device__ __forceinline__ float* slot_of(const Kv4FwdParams& p, long long worke
 template <bool BF16, int D, int NT>
 __global__ void __launch_bounds__(kThreads, (Shape<D, NT>::CtasPerSm)) fa_kv4_fwd_kernel(const Kv4FwdParams p) {
   using Sh = Shape<D, NT>;
-  constexpr int W = Sh::W, ST = Sh::Stages, Block = Sh::Block;
+  constexpr int W = Sh::W, ST = Sh::Stages, Per = Sh::Per, Block = Sh::Block;
   extern __shared__ __align__(128) uint8_t ring_all[];
   __shared__ __align__(8) uint64_t bars[kWarps][ST];
-  __shared__ long long chunk_sum[kThreads + 1], warp_sum[kWarps];
+  __shared__ long long warp_sum[kWarps];
   __shared__ int abort_flag;
+  long long* const chunk_sum = reinterpret_cast<long long*>(ring_all);   // until the first copies
 
   const int lane = threadIdx.x % 32, warp = threadIdx.x / 32, g = lane / 4, t = lane % 4;
-  uint8_t* const ring = ring_all + (size_t)warp * ST * 4 * Block;
-  float4* const fix = reinterpret_cast<float4*>(ring_all + (size_t)kWarps * ST * 4 * Block + warp * Sh::RowBytes) + t;
+  uint8_t* const ring = ring_all + (size_t)warp * ST * Sh::Stage;
+  float4* const fix = reinterpret_cast<float4*>(ring_all + (size_t)kWarps * ST * Sh::Stage + warp * Sh::RowBytes) + t;
   const uint32_t bar0 = smem_u32(&bars[warp][0]), ring0 = smem_u32(ring);
   if (threadIdx.x == 0) abort_flag = 0;
-  if (lane < ST) mbar_init(bar0 + 8 * lane, 4);
+  if (lane < ST) mbar_init(bar0 + 8 * lane, 2 * Per);
   fence_mbar_init();
   grid_dependency_wait();
   grid_dependents_launch();
@@ -198,90 +231,82 @@ __global__ void __launch_bounds__(kThreads, (Shape<D, NT>::CtasPerSm)) fa_kv4_fw
   long long each = (total + workers - 1) / workers;
   if (each < kMinSteps) each = kMinSteps;
   const long long lo = worker * each, hi = lo + each < total ? lo + each : total;
-  if (lo >= hi) {
-    if (lane == 0) p.joins[worker].parts = 0;
-    return;
-  }
-  const long long todo = hi - lo;
-
   int first = 0;   // the last chunk that does not begin behind lo
 #pragma unroll
   for (int i = 0; i < kThreads / 32; ++i) first += __popc(__ballot_sync(0xffffffffu, chunk_sum[32 * i + lane] <= lo));
   --first;
-  Cursor at;
-  at.b = first * per;
-  at.rem = lo - chunk_sum[first];
-  at.r = reach(p, at.b);
+  const long long first_sum = chunk_sum[first];
+  __syncthreads();
+  if (lo >= hi) {
+    if (lane == 0) p.joins[worker].parts = 0;
+    return;
+  }
+  int left = (int)(hi - lo);   // steps (2^31 of them would be hours)
+
+  Cursor at{first * per, lo - first_sum};
   at.settle(p);
 
   // ---- the producer: lane i looks up block i % 2 of step 16 k + i / 2
-  Cursor next = at;
-  next.rem += lane / 2;
-  long long ahead = lane / 2;   // the step that `next` stands on, counted from lo
+  Cursor next{at.b, at.rem + lane / 2};
   int page_next = -1, in_page_next = 0;
   const int per_page_shift = p.c.page_shift - 4;
-  auto look_up = [&]() {
-    page_next = -2;   // no such block: nothing to copy
-    next.settle(p);
-    if (ahead < todo) {
-      const unsigned u = (unsigned)((unsigned long long)next.rem / (unsigned)next.r.steps);
-      const int blk = 2 * (int)(next.rem - (long long)u * next.r.steps) + (lane & 1);
-      if ((long long)blk * kKv4Block < next.r.keys) {
+  auto look_up = [&](bool there) {   // there: the step is this warp's
+    page_next = -2;                  // no such block: nothing to copy
+    const Reach r = next.settle(p);
+    if (there) {
+      const unsigned u = unit_at(next.rem, r.steps);
+      const int blk = 2 * (int)(next.rem - (long long)u * r.steps) + (lane & 1);
+      if ((long long)blk * kKv4Block < r.keys) {
         page_next = p.c.table[(size_t)next.b * p.c.max_pages + (size_t)(blk >> per_page_shift)];
         if (page_next < 0) page_next = -1;
         in_page_next = (int)((u / p.row_tiles) << per_page_shift) + (blk & ((1 << per_page_shift) - 1));
       }
     }
-    ahead += kBatch;
     next.rem += kBatch;
   };
   const uint8_t* src = nullptr;
   uint32_t have = 0;              // which blocks of this batch exist
-  long long to_make = todo;
-  int make_at = 0, make_slot = 0;   // the pair of steps' place in its batch and in the ring
-  auto produce = [&]() {
-    if (make_at == 0) {
+  // The stage that begins `ahead` steps in front of the next one to be taken,
+  // at place `make` of its batch, goes to slot `to`.
+  auto produce = [&](int make, int ahead, int to) {
+    if (make == 0) {
       const bool ok = page_next >= 0 && page_next < p.c.n_pages;
       if (!ok && page_next != -2) atomicCAS(p.c.status, 0, FA_ERR_PAGE);
       src = ok ? p.c.pool + (((size_t)page_next * p.c.Hkv << per_page_shift) + in_page_next) * (size_t)Block : nullptr;
       have = __ballot_sync(0xffffffffu, ok);
-      look_up();
+      look_up(ahead + kBatch + lane / 2 < left);
     }
-    if (lane / 4 == make_at) {
-      const uint32_t bar = bar0 + 8 * make_slot;
+    if (lane / (2 * Per) == make / Per) {
+      const uint32_t bar = bar0 + 8 * to;
       if (src != nullptr) {
         mbar_arrive_expect_tx(bar, Block);
-        bulk_load(ring0 + (make_slot * 4 + lane % 4) * Block, src, Block, bar);
+        bulk_load(ring0 + to * Sh::Stage + lane % (2 * Per) * Block, src, Block, bar);
       } else {
         mbar_arrive(bar);
       }
     }
-    make_at = (make_at + 1) % (kBatch / 2);
-    make_slot ^= 1;
-    to_make -= 2;
   };
-  look_up();
+  look_up(lane / 2 < left);
 #pragma unroll
   for (int i = 0; i < ST; ++i)
-    if (to_make > 0) produce();
+    if (i * Per < left) produce(i * Per, i * Per, i);
 
   const WaitCtx wc{p.wait_limit_ns, &abort_flag, p.c.status};
   Kv4Join join{0, 0, 0};
   const int group = p.H / p.c.Hkv;
   const long long unit_rows = (long long)group * p.T;
-  long long left = todo;
   uint32_t exist = 0;                          // as `have`, from the step to come on
-  int take = 0;                                // the step's place in its batch
+  int take = 0, slot = 0;                      // the step's place in its batch, its stage's in the ring
   uint32_t phase = 0;
   bool alive = true;
-  int flying = 0;                              // pairs of steps on their way when a wait ran out
+  int flying = 0;                              // stages on their way when a wait ran out
 
   while (left > 0 && alive) {
     // ---- one unit's share
-    const Reach r = at.r;
-    const unsigned u = (unsigned)((unsigned long long)at.rem / (unsigned)r.steps);
+    const Reach r = at.settle(p);
+    const unsigned u = unit_at(at.rem, r.steps);
     const int s0 = (int)(at.rem - (long long)u * r.steps);
-    const int s1 = (long long)(r.steps - s0) < left ? r.steps : s0 + (int)left;
+    const int s1 = r.steps - s0 < left ? r.steps : s0 + left;
     const int h = (int)(u / p.row_tiles), tile = (int)(u - (unsigned)h * p.row_tiles);
     const long long row_in = (long long)tile * Sh::Rows;
     const long long row0 = ((long long)at.b * p.H + (long long)h * group) * p.T + row_in;
@@ -346,7 +371,7 @@ __global__ void __launch_bounds__(kThreads, (Shape<D, NT>::CtasPerSm)) fa_kv4_fw
     full_end = __reduce_min_sync(0xffffffffu, full_end);
     last_key = __reduce_max_sync(0xffffffffu, last_key);
 
-    float o[NT][W][2][4], m[NT][2], m_pass[NT][2], l[NT][2];
+    float o[NT][W][2][4], m[NT][2], l[NT][2];
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
 #pragma unroll
@@ -354,28 +379,27 @@ __global__ void __launch_bounds__(kThreads, (Shape<D, NT>::CtasPerSm)) fa_kv4_fw
 #pragma unroll
         for (int i = 0; i < 8; ++i) o[nt][e][i / 4][i % 4] = 0.f;
 #pragma unroll
-      for (int c = 0; c < 2; ++c) m[nt][c] = 0.f, m_pass[nt][c] = -INFINITY, l[nt][c] = 0.f;
+      for (int c = 0; c < 2; ++c) m[nt][c] = kLeast, l[nt][c] = 0.f;
     }
-    float v_up = 1.f, v_pass = 0.f;   // s_V goes in times v_up, and may reach v_pass
+    float v_up = pow2(kMostUp);   // s_V goes in times v_up, up to kVPass
 
-    for (int s = s0; s < s1; ++s) {
-      const int slot = take / 2 % ST;
-      if (take % 2 == 0) {
+    for (int s = s0; s < s1; ++s, --left) {
+      if (take % Per == 0) {
         const uint32_t bar = bar0 + 8 * slot;
         if (!warp_all(mbar_try_wait(bar, phase))) {
           alive = warp_all(mbar_wait(bar, phase, wc));
           if (!alive) {
-            flying = (int)((left - (s - s0) + 1) / 2 - (to_make > 0 ? (to_make + 1) / 2 : 0));
+            flying = min(ST, (left + Per - 1) / Per);
             break;
           }
         }
-        if (take == 0) exist = have;   // the producer is at most ST pairs ahead: in the same batch
+        if (take == 0) exist = have;   // the producer is at most ST stages ahead: in the same batch
       }
       const uint32_t which = exist & 3u;
       exist >>= 2;
       const long long key0 = (long long)s * kStep;
       if (which != 0 && key0 < last_key) {
-        const uint8_t* const base = ring + (slot * 2 + take % 2) * 2 * Block;
+        const uint8_t* const base = ring + slot * Sh::Stage + take % Per * 2 * Block;
         float sc[NT][2][4];
         uint32_t vs[2][2][W / 2];   // V's scales, two to a word
 #pragma unroll
@@ -399,7 +423,7 @@ __global__ void __launch_bounds__(kThreads, (Shape<D, NT>::CtasPerSm)) fa_kv4_fw
             }
 #pragma unroll
             for (int e = 0; e < W; ++e) {
-              sk[half][e] = kv4_scale<BF16>((uint16_t)(raw[e / 2] >> (16 * (e & 1))));
+              sk[half][e] = scale_half<BF16>(raw[e / 2], e & 1);
             }
 #pragma unroll
             for (int e = 0; e < W / 2; ++e) vs[bk][half][e] = raw[W / 2 + e];
@@ -407,9 +431,10 @@ __global__ void __launch_bounds__(kThreads, (Shape<D, NT>::CtasPerSm)) fa_kv4_fw
 #pragma unroll
           for (int e = 0; e < W; ++e) {
             const uint32_t x0 = kw[0][e], x1 = kw[1][e];
-            const uint32_t y0 = x0 >> 8, y1 = x1 >> 8;
+            const uint32_t y0 = __byte_perm(x0, 0, 0x4341), y1 = __byte_perm(x1, 0, 0x4341);
+            const uint32_t z0 = y0 & 0x00f000f0u, z1 = y1 & 0x00f000f0u;
             const uint32_t a0[4] = {x0 & 0x000f000fu, x1 & 0x000f000fu, x0 & 0x00f000f0u, x1 & 0x00f000f0u};
-            const uint32_t a1[4] = {y0 & 0x000f000fu, y1 & 0x000f000fu, y0 & 0x00f000f0u, y1 & 0x00f000f0u};
+            const uint32_t a1[4] = {hsub2(y0, z0), hsub2(y1, z1), z0, z1};
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt) {
               const float4 fx = fix[4 * (nt * W + e)];
@@ -454,38 +479,35 @@ __global__ void __launch_bounds__(kThreads, (Shape<D, NT>::CtasPerSm)) fa_kv4_fw
 #pragma unroll
           for (int e = 0; e < W / 2; ++e) top2 = max_abs2<BF16>(top2, vs[i / 2][i % 2][e]);
         const float v_top = fmaxf(fabsf(kv4_scale<BF16>((uint16_t)top2)), fabsf(kv4_scale<BF16>((uint16_t)(top2 >> 16))));
-        bool pass = v_top > v_pass;
+        bool pass = v_top * v_up > kVPass;
         float top[NT][2];
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
           for (int c = 0; c < 2; ++c) {
-            top[nt][c] = kUnit * fmaxf(fmax3(sc[nt][0][c], sc[nt][0][2 + c], sc[nt][1][c]), sc[nt][1][2 + c]);
-            pass = pass || top[nt][c] > m_pass[nt][c];
+            top[nt][c] = fmaxf(fmax3(sc[nt][0][c], sc[nt][0][2 + c], sc[nt][1][c]), sc[nt][1][2 + c]);
+            pass = pass || fmaf(top[nt][c], kUnit, -m[nt][c]) > kLazy;
           }
         if (__any_sync(0xffffffffu, pass)) {
           float all = v_top;
 #pragma unroll
           for (int d = 16; d; d /= 2) all = fmaxf(all, __shfl_xor_sync(0xffffffffu, all, d));
           float fv = 1.f;
-          if (all > v_pass) {
-            int ex = (int)(__float_as_uint(all) >> 23) - 127;
-            ex = ex < -106 ? -106 : ex;   // P v_up stays finite
-            const float up = pow2(6 - ex);
-            fv = v_pass == 0.f ? 0.f : up / v_up;   // nothing to scale before the first value
+          if (all * v_up > kVPass) {
+            const int ex = 6 + 127 - (int)(__float_as_uint(all) >> 23);   // all * 2^ex in [2^6, 2^7)
+            const float up = pow2(min(ex, kMostUp));
+            fv = up / v_up;
             v_up = up;
-            v_pass = pow2(ex) * 2.f;
           }
 #pragma unroll
           for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
             for (int c = 0; c < 2; ++c) {
-              const float mx = quad_max(top[nt][c]);
+              const float mx = kUnit * quad_max(top[nt][c]);
               float fm = 1.f;
-              if (mx > m_pass[nt][c]) {
-                fm = m_pass[nt][c] == -INFINITY ? 0.f : ex2_approx(m[nt][c] - mx);
+              if (mx - m[nt][c] > kLazy) {
+                fm = ex2_approx(m[nt][c] - mx);
                 m[nt][c] = mx;
-                m_pass[nt][c] = mx + kLazy;
                 l[nt][c] *= fm;
               }
 #pragma unroll
@@ -528,13 +550,13 @@ __global__ void __launch_bounds__(kThreads, (Shape<D, NT>::CtasPerSm)) fa_kv4_fw
 #pragma unroll
           for (int e = 0; e < W; ++e) {
             const uint32_t x0 = vw[0][e], x1 = vw[1][e];
-            const uint32_t y0 = x0 >> 8, y1 = x1 >> 8;
+            const uint32_t y0 = __byte_perm(x0, 0, 0x4341), y1 = __byte_perm(x1, 0, 0x4341);
+            const uint32_t z0 = y0 & 0x00f000f0u, z1 = y1 & 0x00f000f0u;
             const uint32_t a0[4] = {hsub2(x0 & 0x000f000fu, 0x00080008u), hsub2(x0 & 0x00f000f0u, 0x00800080u),
                                     hsub2(x1 & 0x000f000fu, 0x00080008u), hsub2(x1 & 0x00f000f0u, 0x00800080u)};
-            const uint32_t a1[4] = {hsub2(y0 & 0x000f000fu, 0x00080008u), hsub2(y0 & 0x00f000f0u, 0x00800080u),
-                                    hsub2(y1 & 0x000f000fu, 0x00080008u), hsub2(y1 & 0x00f000f0u, 0x00800080u)};
-            const float s0 = kv4_scale<BF16>((uint16_t)(vs[bk][0][e / 2] >> (16 * (e & 1))));
-            const float s1 = kv4_scale<BF16>((uint16_t)(vs[bk][1][e / 2] >> (16 * (e & 1))));
+            const uint32_t a1[4] = {hsub2(hsub2(y0, 0x00080008u), z0), hsub2(z0, 0x00800080u),
+                                    hsub2(hsub2(y1, 0x00080008u), z1), hsub2(z1, 0x00800080u)};
+            const float s0 = scale_half<BF16>(vs[bk][0][e / 2], e & 1), s1 = scale_half<BF16>(vs[bk][1][e / 2], e & 1);
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt) {
               const float(&pr)[4] = sc[nt][bk];
@@ -546,10 +568,11 @@ __global__ void __launch_bounds__(kThreads, (Shape<D, NT>::CtasPerSm)) fa_kv4_fw
           }
         }
       }
-      if (take % 2 != 0) {
+      if (take % Per == Per - 1) {
         __syncwarp();
-        if (to_make > 0) produce();
+        if (left > (ST - 1) * Per + 1) produce((take + 1 + (ST - 1) * Per) % kBatch, (ST - 1) * Per + 1, slot);
         phase ^= slot == ST - 1;
+        slot = slot == ST - 1 ? 0 : slot + 1;
       }
       take = (take + 1) % kBatch;
     }
@@ -558,15 +581,15 @@ __global__ void __launch_bounds__(kThreads, (Shape<D, NT>::CtasPerSm)) fa_kv4_fw
     // ---- the unit's result, or this warp's piece of it
     const bool begins = s0 == 0, ends = s1 == r.steps;
     float* const part = begins && ends ? nullptr : slot_of(p, worker, begins ? 1 : 0, Sh::Slot);
-    const float v_down = v_pass == 0.f ? 0.f : 1.f / v_up;
+    const float v_down = 1.f / v_up;
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
       for (int c = 0; c < 2; ++c) {
         const int row = 8 * nt + 2 * t + c;
-        float ll = quad_sum(l[nt][c]), mm = m_pass[nt][c] == -INFINITY ? -INFINITY : m[nt][c];
+        float ll = quad_sum(l[nt][c]);
         if (row >= rows) continue;
-        if (lim[nt][c] == 0) ll = 0.f, mm = -INFINITY;   // steps that all other rows see whole do not mask this one
+        if (lim[nt][c] == 0) ll = 0.f;   // steps that all other rows see whole do not mask this one
         const float even = ll == 0.f ? 0.f : kUnit / ll, odd = even * 0.0625f;
 #pragma unroll
         for (int e = 0; e < W; ++e) {
@@ -583,9 +606,9 @@ __global__ void __launch_bounds__(kThreads, (Shape<D, NT>::CtasPerSm)) fa_kv4_fw
         }
         if (g == 0) {
           if (part != nullptr)
-            *reinterpret_cast<float2*>(part + Sh::Rows * D + 2 * row) = make_float2(mm, ll);
+            *reinterpret_cast<float2*>(part + Sh::Rows * D + 2 * row) = make_float2(m[nt][c], ll);
           else
-            p.lse[row0 + row] = (mm + log2f(ll)) * 0.69314718055994531f;
+            p.lse[row0 + row] = (m[nt][c] + log2f(ll)) * 0.69314718055994531f;
         }
       }
     if (begins && !ends) {
@@ -594,16 +617,13 @@ __global__ void __launch_bounds__(kThreads, (Shape<D, NT>::CtasPerSm)) fa_kv4_fw
       join.parts = (int)((r.steps - s1 + each - 1) / each);
     }
     at.rem += s1 - s0;
-    left -= s1 - s0;
-    at.settle(p);
   }
   if (!alive) {
     // copies in flight land before the CTA's shared memory goes
     for (; flying > 0; --flying) {
-      const int slot = take / 2 % ST;
       mbar_wait_drain(bar0 + 8 * slot, phase, p.wait_limit_ns);
       phase ^= slot == ST - 1;
-      take = (take + 2) % kBatch;
+      slot = slot == ST - 1 ? 0 : slot + 1;
     }
     join.parts = 0;
   }
@@ -612,7 +632,7 @@ __global__ void __launch_bounds__(kThreads, (Shape<D, NT>::CtasPerSm)) fa_kv4_fw
 
 // O and LSE of the units that lie across workers: one CTA for each worker in
 // which such a unit begins.  Pieces are normalised, with their maximum m (in
-// log2) and sum l beside them; a piece that saw no key has m = -inf, l = 0.
+// log2) and sum l beside them; a piece that saw no key has l = 0.
 // Four elements of a row to a thread; threads to spare take the pieces in
 // turn, eight at a time in flight.
 constexpr int kJoinThreads = 512;
@@ -624,8 +644,7 @@ struct Piece {
   // The two as one; o stays a sum weighted by l.
   __device__ __forceinline__ void add(const float4& x, float xm, float xl) {
     const float top = fmaxf(m, xm);
-    const float fa = m == -INFINITY ? 1.f : ex2_approx(m - top);   // o and l are 0 or NaN while m is -inf
-    const float fb = xm == -INFINITY ? 1.f : ex2_approx(xm - top);
+    const float fa = ex2_approx(m - top), fb = ex2_approx(xm - top);
     o.x = o.x * fa + x.x * fb, o.y = o.y * fa + x.y * fb;
     o.z = o.z * fa + x.z * fb, o.w = o.w * fa + x.w * fb;
     l = l * fa + xl * fb;
@@ -645,7 +664,7 @@ __global__ void __launch_bounds__(kJoinThreads) fa_kv4_join_kernel(const Kv4FwdP
   if (j.parts == 0) return;
   const int items = j.rows * (D / 4), turns = min(kJoinThreads / items, j.parts + 1);
   const int item = threadIdx.x % items, turn = threadIdx.x / items, row = item / (D / 4), col = 4 * (item % (D / 4));
-  Piece mine{make_float4(0.f, 0.f, 0.f, 0.f), -INFINITY, 0.f};
+  Piece mine{make_float4(0.f, 0.f, 0.f, 0.f), kLeast, 0.f};
   if (turn < turns) {
     constexpr int kFly = 8;
     for (int k0 = turn; k0 <= j.parts; k0 += kFly * turns) {
@@ -654,7 +673,7 @@ __global__ void __launch_bounds__(kJoinThreads) fa_kv4_join_kernel(const Kv4FwdP
 #pragma unroll
       for (int i = 0; i < kFly; ++i) {
         const int k = k0 + i * turns;
-        ml[i] = make_float2(-INFINITY, 0.f);
+        ml[i] = make_float2(kLeast, 0.f);
         x[i] = make_float4(0.f, 0.f, 0.f, 0.f);
         if (k <= j.parts) {
           const float* part = slot_of(p, worker + k, k == 0 ? 1 : 0, Sh::Slot);
@@ -711,8 +730,12 @@ cudaError_t launch(Kv4FwdParams p, void* workspace, int sms, cudaStream_t st) {
 }  // namespace
 
 size_t kv4_fwd_workspace(int d, long long rows) {
-  const int nt = row_tiles_of(d, rows), ctas = d / 32 * nt <= 2 ? 4 : d / 32 * nt <= 4 ? 3 : 2;
-  return sizeof(Kv4Join) * kMaxSms * kWarps * 4 + (size_t)kMaxSms * ctas * kWarps * 2 * (8 * nt) * (d + 2) * 4;
+  const int nt = row_tiles_of(d, rows);
+#define FA_KV4(DD, NN) (size_t)Shape<DD, NN>::CtasPerSm * kWarps * 2 * Shape<DD, NN>::Slot * 4
+  const size_t a_sm = d == 128 ? (nt == 1 ? FA_KV4(128, 1) : FA_KV4(128, 2))
+                               : (nt == 1 ? FA_KV4(64, 1) : nt == 2 ? FA_KV4(64, 2) : FA_KV4(64, 4));
+#undef FA_KV4
+  return sizeof(Kv4Join) * kMaxSms * kWarps * 4 + kMaxSms * a_sm;
 }
 
 cudaError_t launch_kv4_fwd(bool bf16, int d, const Kv4FwdParams& p, void* workspace, int sms, cudaStream_t st) {
