@@ -49,9 +49,7 @@ namespace {
 
 constexpr int kWarps = 4;               // of a CTA
 constexpr int kThreads = 32 * kWarps;
-constexpr int kStep = 32;               // keys of a step: two blocks
-constexpr int kBatch = 16;              // steps whose pages a warp looks up at once
-constexpr int kMinSteps = 2;            // least steps worth a warp
+constexpr int kSeen = 128;              // sequences whose lengths a CTA keeps at hand
 constexpr float kUnit = 16777216.f;     // scores and O are summed in units of 2^-24, the subnormals' step
 constexpr float kLeast = -3.402823466e38f;   // a maximum before the first key
 constexpr float kVPass = 128.f;              // with P below 2^8, P s_V stays in fp16's range
@@ -61,13 +59,14 @@ constexpr float kLazy = 8.f;            // log2 by which a score may pass the ru
 template <int D, int NT>
 struct Shape {
   static constexpr int W = D / 32, Rows = 8 * NT, Block = kv4_block_bytes(D);
-  // CTAs a SM, as registers allow, and how its shared memory is cut into
-  // stages: of Per steps each, Stages to a warp.
+  // Blocks of a step, CTAs a SM (as registers allow) and steps on their way to
+  // a warp (as shared memory allows).
+  static constexpr int Blocks = NT == 1 ? 4 : 2, Step = kKv4Block * Blocks;
   static constexpr int CtasPerSm = W * NT <= 2 ? 4 : W * NT <= 4 ? 3 : 2;
-  static constexpr int Per = CtasPerSm == 4 && D == 128 ? 1 : 2, Stages = Per == 1 ? 3 : 2;
+  static constexpr int Stages = CtasPerSm == 3 && D == 128 ? 2 : CtasPerSm == 4 ? 3 : 4;
   static constexpr int Slot = Rows * (D + 2);   // floats of a partial result: O, then m and l by row
   static constexpr int RowBytes = 4 * NT * W * 16;   // per warp: each column pair's factors and offsets
-  static constexpr int Stage = Per * 2 * Block;
+  static constexpr int Stage = Blocks * Block;
   static constexpr size_t Smem = (size_t)kWarps * (Stages * Stage + RowBytes);
 };
 
@@ -136,37 +135,15 @@ __device__ __forceinline__ float quad_sum(float x) {
 
 __device__ __forceinline__ float pow2(int e) { return __int_as_float((e + 127) << 23); }   // -126 <= e <= 127
 
-// How far sequence b reaches in this call.
+// How far a sequence reaches in this call.
 struct Reach {
   int n, keys, steps;   // tokens, keys that the last of them sees, steps of a unit (at least one)
   long long start;
-};
 
-__device__ __forceinline__ Reach reach(const Kv4FwdParams& p, int b) {
-  Reach r;
-  r.n = kv4_count(p.c, b, p.T);
-  r.start = p.c.start[b];
-  const long long end = r.n > 0 ? r.start + r.n : 0, cap = (long long)p.c.max_pages << p.c.page_shift;
-  r.keys = (int)(end < 0 ? 0 : end > cap ? cap : end);
-  r.steps = r.keys > 0 ? (int)(((long long)r.keys + kStep - 1) / kStep) : 1;
-  return r;
-}
-
-// A position in the sequence of all steps: `rem` steps behind the first one of
-// sequence b.  settle moves it on to the sequence that it lies in and returns
-// how far that one reaches.
-struct Cursor {
-  int b;
-  long long rem;
-
-  __device__ __forceinline__ Reach settle(const Kv4FwdParams& p) {
-    Reach r = reach(p, b);
-    while (rem >= (long long)r.steps * p.units_per_seq) {
-      if (b == p.B - 1) break;   // behind the last step
-      rem -= (long long)r.steps * p.units_per_seq;
-      r = reach(p, ++b);
-    }
-    return r;
+  __device__ __forceinline__ Reach(const Kv4FwdParams& p, int first, int count, int step) : n(count), start(first) {
+    const long long end = n > 0 ? start + n : 0, cap = (long long)p.c.max_pages << p.c.page_shift;
+    keys = (int)(end < 0 ? 0 : end > cap ? cap : end);
+    steps = keys > 0 ? (int)(((long long)keys + step - 1) / step) : 1;
   }
 };
 
@@ -183,11 +160,13 @@ __device__ __forceinline__ float* slot_of(const Kv4FwdParams& p, long long worke
 template <bool BF16, int D, int NT>
 __global__ void __launch_bounds__(kThreads, (Shape<D, NT>::CtasPerSm)) fa_kv4_fwd_kernel(const Kv4FwdParams p) {
   using Sh = Shape<D, NT>;
-  constexpr int W = Sh::W, ST = Sh::Stages, Per = Sh::Per, Block = Sh::Block;
+  constexpr int W = Sh::W, ST = Sh::Stages, KB = Sh::Blocks, Block = Sh::Block;
+  constexpr int kBatch = 32 / KB;   // steps whose pages a warp looks up at once
   extern __shared__ __align__(128) uint8_t ring_all[];
   __shared__ __align__(8) uint64_t bars[kWarps][ST];
   __shared__ long long warp_sum[kWarps];
   __shared__ int abort_flag;
+  __shared__ int2 seen[kSeen];   // start and count
   long long* const chunk_sum = reinterpret_cast<long long*>(ring_all);   // until the first copies
 
   const int lane = threadIdx.x % 32, warp = threadIdx.x / 32, g = lane / 4, t = lane % 4;
@@ -195,7 +174,7 @@ __global__ void __launch_bounds__(kThreads, (Shape<D, NT>::CtasPerSm)) fa_kv4_fw
   float4* const fix = reinterpret_cast<float4*>(ring_all + (size_t)kWarps * ST * Sh::Stage + warp * Sh::RowBytes) + t;
   const uint32_t bar0 = smem_u32(&bars[warp][0]), ring0 = smem_u32(ring);
   if (threadIdx.x == 0) abort_flag = 0;
-  if (lane < ST) mbar_init(bar0 + 8 * lane, 2 * Per);
+  if (lane < ST) mbar_init(bar0 + 8 * lane, KB);
   fence_mbar_init();
   grid_dependency_wait();
   grid_dependents_launch();
@@ -204,7 +183,7 @@ __global__ void __launch_bounds__(kThreads, (Shape<D, NT>::CtasPerSm)) fa_kv4_fw
   const int per = (p.B + kThreads - 1) / kThreads;
   long long mine = 0;
   for (int i = 0, b = threadIdx.x * per; i < per && b < p.B; ++i, ++b) {
-    const Reach r = reach(p, b);
+    const Reach r(p, p.c.start[b], kv4_count(p.c, b, p.T), Sh::Step);
     mine += r.steps;
     if (blockIdx.x == 0 && r.n > 0 && r.start + r.n > r.keys && r.start + r.n > 0)   // past the page table
       atomicCAS(p.c.status, 0, FA_ERR_PAGE);
@@ -228,14 +207,19 @@ __global__ void __launch_bounds__(kThreads, (Shape<D, NT>::CtasPerSm)) fa_kv4_fw
   __syncthreads();
 
   const long long workers = (long long)gridDim.x * kWarps, worker = (long long)blockIdx.x * kWarps + warp;
-  long long each = (total + workers - 1) / workers;
-  if (each < kMinSteps) each = kMinSteps;
+  const long long each = (total + workers - 1) / workers;
   const long long lo = worker * each, hi = lo + each < total ? lo + each : total;
-  int first = 0;   // the last chunk that does not begin behind lo
+  // the last chunk of sequences that does not begin behind a step
+  auto chunk_of = [&](long long step) {
+    int n = 0;
 #pragma unroll
-  for (int i = 0; i < kThreads / 32; ++i) first += __popc(__ballot_sync(0xffffffffu, chunk_sum[32 * i + lane] <= lo));
-  --first;
+    for (int i = 0; i < kThreads / 32; ++i) n += __popc(__ballot_sync(0xffffffffu, chunk_sum[32 * i + lane] <= step));
+    return n - 1;
+  };
+  const int first = chunk_of(lo), b_seen = chunk_of(lo - warp * each) * per;
   const long long first_sum = chunk_sum[first];
+  for (int i = threadIdx.x; i < kSeen && b_seen + i < p.B; i += kThreads)
+    seen[i] = make_int2(p.c.start[b_seen + i], kv4_count(p.c, b_seen + i, p.T));
   __syncthreads();
   if (lo >= hi) {
     if (lane == 0) p.joins[worker].parts = 0;
@@ -243,19 +227,41 @@ __global__ void __launch_bounds__(kThreads, (Shape<D, NT>::CtasPerSm)) fa_kv4_fw
   }
   int left = (int)(hi - lo);   // steps (2^31 of them would be hours)
 
+  // A position in the sequence of all steps: `rem` steps behind the first one
+  // of sequence b.  settle moves it on to the sequence that it lies in.
+  struct Cursor {
+    int b;
+    long long rem;
+  };
+  auto reach = [&](int b) {
+    const int i = b - b_seen;
+    const int2 x = i < kSeen ? seen[i] : make_int2(p.c.start[b], kv4_count(p.c, b, p.T));
+    return Reach(p, x.x, x.y, Sh::Step);
+  };
+  auto settle = [&](Cursor& c) {
+    Reach r = reach(c.b);
+    while (c.rem >= (long long)r.steps * p.units_per_seq) {
+      if (c.b == p.B - 1) break;   // behind the last step
+      c.rem -= (long long)r.steps * p.units_per_seq;
+      r = reach(++c.b);
+    }
+    return r;
+  };
   Cursor at{first * per, lo - first_sum};
-  at.settle(p);
+  settle(at);
 
-  // ---- the producer: lane i looks up block i % 2 of step 16 k + i / 2
-  Cursor next{at.b, at.rem + lane / 2};
+  // ---- the producer: lane i looks up block i % KB of step kBatch k + i / KB
+  const int my_step = lane / KB;
+  const uint32_t my_dst = ring0 + lane % KB * Block;
+  Cursor next{at.b, at.rem + my_step};
   int page_next = -1, in_page_next = 0;
   const int per_page_shift = p.c.page_shift - 4;
   auto look_up = [&](bool there) {   // there: the step is this warp's
     page_next = -2;                  // no such block: nothing to copy
-    const Reach r = next.settle(p);
+    const Reach r = settle(next);
     if (there) {
       const unsigned u = unit_at(next.rem, r.steps);
-      const int blk = 2 * (int)(next.rem - (long long)u * r.steps) + (lane & 1);
+      const int blk = KB * (int)(next.rem - (long long)u * r.steps) + lane % KB;
       if ((long long)blk * kKv4Block < r.keys) {
         page_next = p.c.table[(size_t)next.b * p.c.max_pages + (size_t)(blk >> per_page_shift)];
         if (page_next < 0) page_next = -1;
@@ -265,31 +271,28 @@ __global__ void __launch_bounds__(kThreads, (Shape<D, NT>::CtasPerSm)) fa_kv4_fw
     next.rem += kBatch;
   };
   const uint8_t* src = nullptr;
+  uint32_t bytes = 0;             // to copy: a block, or none
   uint32_t have = 0;              // which blocks of this batch exist
-  // The stage that begins `ahead` steps in front of the next one to be taken,
-  // at place `make` of its batch, goes to slot `to`.
+  // The step `ahead` steps in front of the one at hand, at place `make` of its
+  // batch, goes to stage `to`.
   auto produce = [&](int make, int ahead, int to) {
     if (make == 0) {
       const bool ok = page_next >= 0 && page_next < p.c.n_pages;
       if (!ok && page_next != -2) atomicCAS(p.c.status, 0, FA_ERR_PAGE);
-      src = ok ? p.c.pool + (((size_t)page_next * p.c.Hkv << per_page_shift) + in_page_next) * (size_t)Block : nullptr;
+      bytes = ok ? Block : 0;
+      src = p.c.pool + (((size_t)(ok ? page_next : 0) * p.c.Hkv << per_page_shift) + in_page_next) * (size_t)Block;
       have = __ballot_sync(0xffffffffu, ok);
-      look_up(ahead + kBatch + lane / 2 < left);
+      look_up(ahead + kBatch + my_step < left);
     }
-    if (lane / (2 * Per) == make / Per) {
-      const uint32_t bar = bar0 + 8 * to;
-      if (src != nullptr) {
-        mbar_arrive_expect_tx(bar, Block);
-        bulk_load(ring0 + to * Sh::Stage + lane % (2 * Per) * Block, src, Block, bar);
-      } else {
-        mbar_arrive(bar);
-      }
+    if (my_step == make) {
+      mbar_arrive_expect_tx(bar0 + 8 * to, bytes);
+      if (bytes != 0) bulk_load(my_dst + to * Sh::Stage, src, Block, bar0 + 8 * to);
     }
   };
-  look_up(lane / 2 < left);
+  look_up(my_step < left);
 #pragma unroll
   for (int i = 0; i < ST; ++i)
-    if (i * Per < left) produce(i * Per, i * Per, i);
+    if (i < left) produce(i, i, i);
 
   const WaitCtx wc{p.wait_limit_ns, &abort_flag, p.c.status};
   Kv4Join join{0, 0, 0};
@@ -303,7 +306,7 @@ __global__ void __launch_bounds__(kThreads, (Shape<D, NT>::CtasPerSm)) fa_kv4_fw
 
   while (left > 0 && alive) {
     // ---- one unit's share
-    const Reach r = at.settle(p);
+    const Reach r = settle(at);
     const unsigned u = unit_at(at.rem, r.steps);
     const int s0 = (int)(at.rem - (long long)u * r.steps);
     const int s1 = r.steps - s0 < left ? r.steps : s0 + left;
@@ -314,7 +317,7 @@ __global__ void __launch_bounds__(kThreads, (Shape<D, NT>::CtasPerSm)) fa_kv4_fw
 
     uint32_t qb[NT][W][4];
     int lim[NT][2];
-    int full_end = 0x7fffffff, last_key = 0;
+    unsigned full_end = 0x7fffffffu, last_key = 0;
     const long long cap = (long long)p.c.max_pages << p.c.page_shift;
     auto limit_of = [&](int row) -> int {
       if (row >= rows) return 0;
@@ -362,8 +365,8 @@ __global__ void __launch_bounds__(kThreads, (Shape<D, NT>::CtasPerSm)) fa_kv4_fw
         __syncwarp();
         fix[4 * (nt * W + e)] = both;   // all lanes of a column pair write the same
       }
-      if (my_lim > 0) full_end = min(full_end, my_lim);
-      last_key = max(last_key, my_lim);
+      if (my_lim > 0) full_end = min(full_end, (unsigned)my_lim);
+      last_key = max(last_key, (unsigned)my_lim);
       lim[nt][0] = __shfl_sync(0xffffffffu, my_lim, 8 * t);
       lim[nt][1] = __shfl_sync(0xffffffffu, my_lim, 8 * t + 4);
     }
@@ -384,26 +387,24 @@ __global__ void __launch_bounds__(kThreads, (Shape<D, NT>::CtasPerSm)) fa_kv4_fw
     float v_up = pow2(kMostUp);   // s_V goes in times v_up, up to kVPass
 
     for (int s = s0; s < s1; ++s, --left) {
-      if (take % Per == 0) {
-        const uint32_t bar = bar0 + 8 * slot;
-        if (!warp_all(mbar_try_wait(bar, phase))) {
-          alive = warp_all(mbar_wait(bar, phase, wc));
-          if (!alive) {
-            flying = min(ST, (left + Per - 1) / Per);
-            break;
-          }
+      const uint32_t bar = bar0 + 8 * slot;
+      if (!warp_all(mbar_try_wait(bar, phase))) {
+        alive = warp_all(mbar_wait(bar, phase, wc));
+        if (!alive) {
+          flying = min(ST, left);
+          break;
         }
-        if (take == 0) exist = have;   // the producer is at most ST stages ahead: in the same batch
       }
-      const uint32_t which = exist & 3u;
-      exist >>= 2;
-      const long long key0 = (long long)s * kStep;
+      if (take == 0) exist = have;   // the producer is at most ST steps ahead: in the same batch
+      const uint32_t which = exist & ((1u << KB) - 1);
+      exist >>= KB;
+      const unsigned key0 = (unsigned)s * Sh::Step;
       if (which != 0 && key0 < last_key) {
-        const uint8_t* const base = ring + slot * Sh::Stage + take % Per * 2 * Block;
-        float sc[NT][2][4];
-        uint32_t vs[2][2][W / 2];   // V's scales, two to a word
+        uint8_t* const base = ring + slot * Sh::Stage;
+        float sc[NT][KB][4];
+        uint32_t top2 = 0;   // V's scales: the largest magnitudes in even and odd groups
 #pragma unroll
-        for (int bk = 0; bk < 2; ++bk) {
+        for (int bk = 0; bk < KB; ++bk) {
           const uint8_t* blk = base + bk * Block;
           float sk[2][W];
           uint32_t kw[2][W];
@@ -422,11 +423,9 @@ __global__ void __launch_bounds__(kThreads, (Shape<D, NT>::CtasPerSm)) fa_kv4_fw
               raw[0] = y.x, raw[1] = y.y;
             }
 #pragma unroll
-            for (int e = 0; e < W; ++e) {
-              sk[half][e] = scale_half<BF16>(raw[e / 2], e & 1);
-            }
+            for (int e = 0; e < W; ++e) sk[half][e] = scale_half<BF16>(raw[e / 2], e & 1);
 #pragma unroll
-            for (int e = 0; e < W / 2; ++e) vs[bk][half][e] = raw[W / 2 + e];
+            for (int e = 0; e < W / 2; ++e) top2 = max_abs2<BF16>(top2, raw[W / 2 + e]);
           }
 #pragma unroll
           for (int e = 0; e < W; ++e) {
@@ -453,31 +452,34 @@ __global__ void __launch_bounds__(kThreads, (Shape<D, NT>::CtasPerSm)) fa_kv4_fw
             }
           }
         }
-        if (which != 3u || key0 + kStep > full_end) {
-          // keys that a row does not see; scales behind the last key may be anything
+        if (which != (1u << KB) - 1 || key0 + Sh::Step > full_end) {
+          // keys that a row does not see; V's scales behind the last key may be
+          // anything, and become 0
+          top2 = 0;
 #pragma unroll
-          for (int bk = 0; bk < 2; ++bk)
+          for (int bk = 0; bk < KB; ++bk)
 #pragma unroll
             for (int half = 0; half < 2; ++half) {
-              const long long key = key0 + 16 * bk + 8 * half + g;
+              const unsigned key = key0 + 16 * bk + 8 * half + g;
               const bool there = (which >> bk & 1u) != 0;
-              if (!there || key >= last_key) {
+              uint32_t* const vs = reinterpret_cast<uint32_t*>(base + bk * Block + 16 * D) + (half * 8 + g) * W + W / 2;
 #pragma unroll
-                for (int e = 0; e < W / 2; ++e) vs[bk][half][e] = 0;
+              for (int e = 0; e < W / 2; ++e) {
+                if (there && key < last_key)
+                  top2 = max_abs2<BF16>(top2, vs[e]);
+                else if (t == 0)
+                  vs[e] = 0;
               }
 #pragma unroll
               for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
                 for (int c = 0; c < 2; ++c)
-                  if (!there || key >= lim[nt][c]) sc[nt][bk][2 * half + c] = -INFINITY;
+                  if (!there || key >= (unsigned)lim[nt][c]) sc[nt][bk][2 * half + c] = -INFINITY;
             }
+          fence_async_smem();   // before the next copy to this stage
+          __syncwarp();
         }
-        // ---- V's scales, relative to the largest so far
-        uint32_t top2 = 0;
-#pragma unroll
-        for (int i = 0; i < 4; ++i)
-#pragma unroll
-          for (int e = 0; e < W / 2; ++e) top2 = max_abs2<BF16>(top2, vs[i / 2][i % 2][e]);
+        // ---- V's scales go in relative to the largest so far
         const float v_top = fmaxf(fabsf(kv4_scale<BF16>((uint16_t)top2)), fabsf(kv4_scale<BF16>((uint16_t)(top2 >> 16))));
         bool pass = v_top * v_up > kVPass;
         float top[NT][2];
@@ -485,7 +487,9 @@ __global__ void __launch_bounds__(kThreads, (Shape<D, NT>::CtasPerSm)) fa_kv4_fw
         for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
           for (int c = 0; c < 2; ++c) {
-            top[nt][c] = fmaxf(fmax3(sc[nt][0][c], sc[nt][0][2 + c], sc[nt][1][c]), sc[nt][1][2 + c]);
+            top[nt][c] = fmaxf(sc[nt][0][c], sc[nt][0][2 + c]);
+#pragma unroll
+            for (int bk = 1; bk < KB; ++bk) top[nt][c] = fmax3(top[nt][c], sc[nt][bk][c], sc[nt][bk][2 + c]);
             pass = pass || fmaf(top[nt][c], kUnit, -m[nt][c]) > kLazy;
           }
         if (__any_sync(0xffffffffu, pass)) {
@@ -522,7 +526,7 @@ __global__ void __launch_bounds__(kThreads, (Shape<D, NT>::CtasPerSm)) fa_kv4_fw
           uint64_t sum = f2_pack(l[nt][0], l[nt][1]);
           const uint64_t neg = f2_pack(-m[nt][0], -m[nt][1]);
 #pragma unroll
-          for (int i = 0; i < 4; ++i) {
+          for (int i = 0; i < 2 * KB; ++i) {
             float(&x)[4] = sc[nt][i / 2];
             float x0, x1;
             f2_unpack(f2_fma(f2_pack(x[2 * (i % 2)], x[2 * (i % 2) + 1]), f2_pack(kUnit, kUnit), neg), x0, x1);
@@ -534,17 +538,20 @@ __global__ void __launch_bounds__(kThreads, (Shape<D, NT>::CtasPerSm)) fa_kv4_fw
         }
         // ---- O^T += V^T P^T
 #pragma unroll
-        for (int bk = 0; bk < 2; ++bk) {
+        for (int bk = 0; bk < KB; ++bk) {
           const uint8_t* blk = base + bk * Block + 8 * D;
-          uint32_t vw[2][W];
+          uint32_t vw[2][W], vs[2][W / 2];
 #pragma unroll
           for (int half = 0; half < 2; ++half) {
             if constexpr (W == 4) {
+              const uint2 y = reinterpret_cast<const uint2*>(blk + 8 * D)[2 * (half * 8 + g) + 1];
+              vs[half][0] = y.x, vs[half][1] = y.y;
               const uint4 x = reinterpret_cast<const uint4*>(blk)[half * 32 + lane];
               vw[half][0] = x.x, vw[half][1] = x.y, vw[half][2] = x.z, vw[half][3] = x.w;
             } else {
               const uint2 x = reinterpret_cast<const uint2*>(blk)[half * 32 + lane];
               vw[half][0] = x.x, vw[half][1] = x.y;
+              vs[half][0] = reinterpret_cast<const uint32_t*>(blk + 8 * D)[2 * (half * 8 + g) + 1];
             }
           }
 #pragma unroll
@@ -556,7 +563,7 @@ __global__ void __launch_bounds__(kThreads, (Shape<D, NT>::CtasPerSm)) fa_kv4_fw
                                     hsub2(x1 & 0x000f000fu, 0x00080008u), hsub2(x1 & 0x00f000f0u, 0x00800080u)};
             const uint32_t a1[4] = {hsub2(hsub2(y0, 0x00080008u), z0), hsub2(z0, 0x00800080u),
                                     hsub2(hsub2(y1, 0x00080008u), z1), hsub2(z1, 0x00800080u)};
-            const float s0 = scale_half<BF16>(vs[bk][0][e / 2], e & 1), s1 = scale_half<BF16>(vs[bk][1][e / 2], e & 1);
+            const float s0 = scale_half<BF16>(vs[0][e / 2], e & 1), s1 = scale_half<BF16>(vs[1][e / 2], e & 1);
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt) {
               const float(&pr)[4] = sc[nt][bk];
@@ -568,12 +575,10 @@ __global__ void __launch_bounds__(kThreads, (Shape<D, NT>::CtasPerSm)) fa_kv4_fw
           }
         }
       }
-      if (take % Per == Per - 1) {
-        __syncwarp();
-        if (left > (ST - 1) * Per + 1) produce((take + 1 + (ST - 1) * Per) % kBatch, (ST - 1) * Per + 1, slot);
-        phase ^= slot == ST - 1;
-        slot = slot == ST - 1 ? 0 : slot + 1;
-      }
+      __syncwarp();
+      if (left > ST) produce((take + ST) % kBatch, ST, slot);
+      phase ^= slot == ST - 1;
+      slot = slot == ST - 1 ? 0 : slot + 1;
       take = (take + 1) % kBatch;
     }
     if (!alive) break;
