@@ -159,7 +159,10 @@ struct Kv4FwdParams {
   // set by the launch
   int row_tiles;             // tiles of query rows a key head
   long long units_per_seq;   // Hkv * row_tiles
-  Kv4Join* joins;            // [workers]
+  int workers;               // warps of the grid
+  int join_units;            // joins go by unit, else by worker
+  int join_items;            // fours of elements a CTA of the joining kernel
+  Kv4Join* joins;            // [units or workers]
   float* partials;           // [workers][2] pieces of results
 };
 

@@ -16,16 +16,17 @@
 // ring that belongs to the warp, ST steps deep, so no warp waits for another.
 //   S^T = K Q^T by mma.m16n8k16, keys as rows and 8 query rows as columns:
 //     nothing is wasted when four or eight query heads share a key head.  A
-//     code c = n + 8 enters as the fp16 subnormal that its nibble is, and 8
-//     times the sum of q is taken off each group's sum of 32, which is then
-//     scaled in float32.  q goes in as fp16, brought to 2^14 .. 2^15 per row
-//     and group by a power of two that the scale takes back (elements 2^21
-//     below the group's largest round, relative to it, at 2^-36).
+//     code c = n + 8 enters as the fp16 subnormal that its nibble is; each
+//     group's sum of 32 starts at -8 times the sum of q and is then scaled in
+//     float32.  q goes in as fp16, its row's largest element brought to
+//     2^14 .. 2^15 by a power of two that the scale takes back: elements 2^-21
+//     of the row's largest or less round at 2^-36 of it.
 //   O^T = V^T P^T: the head's elements as rows.  V's codes become n by one
-//     fp16 subtraction (exact: a sum over many keys must not carry an offset);
-//     P s_V is rounded to fp16, with s_V taken relative to the largest one so
-//     far (a power of two, which O's end takes back).  P s_V changes from
-//     accumulator to operand order by movmatrix.
+//     fp16 subtraction, exactly: a sum over many keys must not carry an offset
+//     (taking it back by a product with -8 measured 6% slower).  P s_V is
+//     rounded to fp16, with s_V taken relative to the largest one so far (a
+//     power of two, which O's end takes back), and changes from accumulator to
+//     operand order by movmatrix.
 // The running maximum moves only when a score passes it by 2^8: P stays below
 // 2^8 and P s_V below 2^15.
 #include <cuda_runtime.h>
@@ -37,12 +38,12 @@
 
 namespace fa {
 
-// What the joining kernel needs to know of the unit that begins in a worker's
-// range and ends behind it (parts = 0: there is none).
+// What the joining kernel needs to know of a unit that ends behind the range
+// of the worker in which it begins (parts = 0 for others).
 struct Kv4Join {
   long long row;   // first row of the unit in O and LSE
   int rows;
-  int parts;       // pieces in the workers that follow
+  int worker, parts;   // the worker, and how many pieces follow in those behind it
 };
 
 namespace {
@@ -65,7 +66,7 @@ struct Shape {
   static constexpr int CtasPerSm = W * NT <= 2 ? 4 : W * NT <= 4 ? 3 : 2;
   static constexpr int Stages = CtasPerSm == 3 && D == 128 ? 2 : CtasPerSm == 4 ? 3 : 4;
   static constexpr int Slot = Rows * (D + 2);   // floats of a partial result: O, then m and l by row
-  static constexpr int RowBytes = 4 * NT * W * 16;   // per warp: each column pair's factors and offsets
+  static constexpr int RowBytes = 4 * NT * W * 16;   // per warp: what is taken off the scores of each column pair
   static constexpr int Stage = Blocks * Block;
   static constexpr size_t Smem = (size_t)kWarps * (Stages * Stage + RowBytes);
 };
@@ -171,7 +172,7 @@ __global__ void __launch_bounds__(kThreads, (Shape<D, NT>::CtasPerSm)) fa_kv4_fw
 
   const int lane = threadIdx.x % 32, warp = threadIdx.x / 32, g = lane / 4, t = lane % 4;
   uint8_t* const ring = ring_all + (size_t)warp * ST * Sh::Stage;
-  float4* const fix = reinterpret_cast<float4*>(ring_all + (size_t)kWarps * ST * Sh::Stage + warp * Sh::RowBytes) + t;
+  float4* const less = reinterpret_cast<float4*>(ring_all + (size_t)kWarps * ST * Sh::Stage + warp * Sh::RowBytes) + t;
   const uint32_t bar0 = smem_u32(&bars[warp][0]), ring0 = smem_u32(ring);
   if (threadIdx.x == 0) abort_flag = 0;
   if (lane < ST) mbar_init(bar0 + 8 * lane, KB);
@@ -206,7 +207,7 @@ __global__ void __launch_bounds__(kThreads, (Shape<D, NT>::CtasPerSm)) fa_kv4_fw
   chunk_sum[threadIdx.x] = before + incl - mine;
   __syncthreads();
 
-  const long long workers = (long long)gridDim.x * kWarps, worker = (long long)blockIdx.x * kWarps + warp;
+  const long long workers = p.workers, worker = (long long)blockIdx.x * kWarps + warp;
   const long long each = (total + workers - 1) / workers;
   const long long lo = worker * each, hi = lo + each < total ? lo + each : total;
   // the last chunk of sequences that does not begin behind a step
@@ -222,7 +223,7 @@ __global__ void __launch_bounds__(kThreads, (Shape<D, NT>::CtasPerSm)) fa_kv4_fw
     seen[i] = make_int2(p.c.start[b_seen + i], kv4_count(p.c, b_seen + i, p.T));
   __syncthreads();
   if (lo >= hi) {
-    if (lane == 0) p.joins[worker].parts = 0;
+    if (lane == 0 && !p.join_units) p.joins[worker].parts = 0;
     return;
   }
   int left = (int)(hi - lo);   // steps (2^31 of them would be hours)
@@ -295,7 +296,7 @@ __global__ void __launch_bounds__(kThreads, (Shape<D, NT>::CtasPerSm)) fa_kv4_fw
     if (i < left) produce(i, i, i);
 
   const WaitCtx wc{p.wait_limit_ns, &abort_flag, p.c.status};
-  Kv4Join join{0, 0, 0};
+  Kv4Join join{0, 0, 0, 0};
   const int group = p.H / p.c.Hkv;
   const long long unit_rows = (long long)group * p.T;
   uint32_t exist = 0;                          // as `have`, from the step to come on
@@ -304,7 +305,7 @@ __global__ void __launch_bounds__(kThreads, (Shape<D, NT>::CtasPerSm)) fa_kv4_fw
   bool alive = true;
   int flying = 0;                              // stages on their way when a wait ran out
 
-  while (left > 0 && alive) {
+  while (left > 0) {
     // ---- one unit's share
     const Reach r = settle(at);
     const unsigned u = unit_at(at.rem, r.steps);
@@ -314,8 +315,18 @@ __global__ void __launch_bounds__(kThreads, (Shape<D, NT>::CtasPerSm)) fa_kv4_fw
     const long long row_in = (long long)tile * Sh::Rows;
     const long long row0 = ((long long)at.b * p.H + (long long)h * group) * p.T + row_in;
     const int rows = unit_rows - row_in < Sh::Rows ? (int)(unit_rows - row_in) : Sh::Rows;
+    const bool begins = s0 == 0, ends = s1 == r.steps;
+    const int left_then = left - (s1 - s0);
+    const long long unit = (long long)at.b * p.units_per_seq + u;
+    at.rem += s1 - s0;
+    if (!alive) {   // a wait ran out before: nothing to join
+      if (begins && p.join_units && lane == 0) p.joins[unit].parts = 0;
+      left = left_then;
+      continue;
+    }
 
     uint32_t qb[NT][W][4];
+    float f[NT][2];   // of the rows of this lane's columns
     int lim[NT][2];
     unsigned full_end = 0x7fffffffu, last_key = 0;
     const long long cap = (long long)p.c.max_pages << p.c.page_shift;
@@ -330,25 +341,30 @@ __global__ void __launch_bounds__(kThreads, (Shape<D, NT>::CtasPerSm)) fa_kv4_fw
     for (int nt = 0; nt < NT; ++nt) {
       const int my_lim = limit_of(8 * nt + g);
       const uint4* qr = reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(p.q) + (row0 + 8 * nt + g) * D) + t;
+      uint4 raw[W];
+#pragma unroll
+      for (int e = 0; e < W; ++e) raw[e] = my_lim > 0 ? qr[4 * e] : make_uint4(0, 0, 0, 0);
+      uint32_t most = 0;
+#pragma unroll
+      for (int e = 0; e < W; ++e)
+        most = max_abs2<BF16>(most, max_abs2<BF16>(max_abs2<BF16>(raw[e].x, raw[e].y), max_abs2<BF16>(raw[e].z, raw[e].w)));
+      float top = fmaxf(fabsf(kv4_scale<BF16>((uint16_t)most)), fabsf(kv4_scale<BF16>((uint16_t)(most >> 16))));
+      top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
+      top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
+      int ex = 14 + 127 - (int)(__float_as_uint(top) >> 23);   // top * 2^ex in [2^14, 2^15)
+      ex = ex > 100 ? 100 : ex;
+      const float up = pow2(ex), back = fminf(p.scale_log2 * kUnit * pow2(-ex), 3e38f);
+      f[nt][0] = __shfl_sync(0xffffffffu, back, 8 * t);
+      f[nt][1] = __shfl_sync(0xffffffffu, back, 8 * t + 4);
 #pragma unroll
       for (int e = 0; e < W; ++e) {
-        uint4 x = make_uint4(0, 0, 0, 0);
-        if (my_lim > 0) x = qr[4 * e];
         float v[8];
-        const uint32_t xs[4] = {x.x, x.y, x.z, x.w};
+        const uint32_t xs[4] = {raw[e].x, raw[e].y, raw[e].z, raw[e].w};
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-          v[2 * i] = kv4_scale<BF16>((uint16_t)(xs[i] & 0xffffu));
-          v[2 * i + 1] = kv4_scale<BF16>((uint16_t)(xs[i] >> 16));
+          v[2 * i] = scale_half<BF16>(xs[i], 0);
+          v[2 * i + 1] = scale_half<BF16>(xs[i], 1);
         }
-        float top = 0.f;
-#pragma unroll
-        for (int i = 0; i < 8; ++i) top = fmaxf(top, fabsf(v[i]));
-        top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
-        top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
-        int ex = 14 + 127 - (int)(__float_as_uint(top) >> 23);   // top * 2^ex in [2^14, 2^15)
-        ex = ex > 100 ? 100 : ex;
-        const float up = pow2(ex), back = p.scale_log2 * pow2(-ex);
         float even = 0.f, odd = 0.f;
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
@@ -357,13 +373,12 @@ __global__ void __launch_bounds__(kThreads, (Shape<D, NT>::CtasPerSm)) fa_kv4_fw
           const float2 y = __half22float2(*reinterpret_cast<__half2*>(&qb[nt][e][i]));
           (i & 1 ? odd : even) += y.x + y.y;
         }
-        float c = -8.f / 16777216.f * back * (even + 16.f * odd);
+        float c = -8.f / kUnit * (even + 16.f * odd);
         c += __shfl_xor_sync(0xffffffffu, c, 1);
         c += __shfl_xor_sync(0xffffffffu, c, 2);
-        const float4 both = make_float4(__shfl_sync(0xffffffffu, back, 8 * t), __shfl_sync(0xffffffffu, back, 8 * t + 4),
-                                        __shfl_sync(0xffffffffu, c, 8 * t), __shfl_sync(0xffffffffu, c, 8 * t + 4));
+        const float c0 = __shfl_sync(0xffffffffu, c, 8 * t), c1 = __shfl_sync(0xffffffffu, c, 8 * t + 4);
         __syncwarp();
-        fix[4 * (nt * W + e)] = both;   // all lanes of a column pair write the same
+        less[4 * (nt * W + e)] = make_float4(c0, c1, c0, c1);   // all lanes of a column pair write the same
       }
       if (my_lim > 0) full_end = min(full_end, (unsigned)my_lim);
       last_key = max(last_key, (unsigned)my_lim);
@@ -427,30 +442,34 @@ __global__ void __launch_bounds__(kThreads, (Shape<D, NT>::CtasPerSm)) fa_kv4_fw
 #pragma unroll
             for (int e = 0; e < W / 2; ++e) top2 = max_abs2<BF16>(top2, raw[W / 2 + e]);
           }
+          // the groups' products side by side, so that none waits for another
+          float d[NT][W][4];
 #pragma unroll
           for (int e = 0; e < W; ++e) {
             const uint32_t x0 = kw[0][e], x1 = kw[1][e];
-            const uint32_t y0 = __byte_perm(x0, 0, 0x4341), y1 = __byte_perm(x1, 0, 0x4341);
-            const uint32_t z0 = y0 & 0x00f000f0u, z1 = y1 & 0x00f000f0u;
-            const uint32_t a0[4] = {x0 & 0x000f000fu, x1 & 0x000f000fu, x0 & 0x00f000f0u, x1 & 0x00f000f0u};
-            const uint32_t a1[4] = {hsub2(y0, z0), hsub2(y1, z1), z0, z1};
+            const uint32_t a[4] = {x0 & 0x000f000fu, x1 & 0x000f000fu, x0 & 0x00f000f0u, x1 & 0x00f000f0u};
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt) {
-              const float4 fx = fix[4 * (nt * W + e)];
-              const float none[4] = {0.f, 0.f, 0.f, 0.f};
-              float d[4];
-              mma16816(d, a0, qb[nt][e][0], qb[nt][e][1], none);
-              mma16816(d, a1, qb[nt][e][2], qb[nt][e][3], d);
-#pragma unroll
-              for (int half = 0; half < 2; ++half) {
-                float x0, x1;
-                f2_unpack(f2_fma(f2_pack(d[2 * half], d[2 * half + 1]), f2_pack(fx.x, fx.y), f2_pack(fx.z, fx.w)), x0, x1);
-                float(&out)[4] = sc[nt][bk];
-                out[2 * half] = e == 0 ? x0 * sk[half][0] : fmaf(x0, sk[half][e], out[2 * half]);
-                out[2 * half + 1] = e == 0 ? x1 * sk[half][0] : fmaf(x1, sk[half][e], out[2 * half + 1]);
-              }
+              const float4 c = less[4 * (nt * W + e)];
+              const float c4[4] = {c.x, c.y, c.z, c.w};
+              mma16816(d[nt][e], a, qb[nt][e][0], qb[nt][e][1], c4);
             }
           }
+#pragma unroll
+          for (int e = 0; e < W; ++e) {
+            const uint32_t y0 = __byte_perm(kw[0][e], 0, 0x4341), y1 = __byte_perm(kw[1][e], 0, 0x4341);
+            const uint32_t z0 = y0 & 0x00f000f0u, z1 = y1 & 0x00f000f0u;
+            const uint32_t a[4] = {hsub2(y0, z0), hsub2(y1, z1), z0, z1};
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt) mma16816(d[nt][e], a, qb[nt][e][2], qb[nt][e][3], d[nt][e]);
+          }
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+            for (int e = 0; e < W; ++e)
+#pragma unroll
+              for (int i = 0; i < 4; ++i)
+                sc[nt][bk][i] = e == 0 ? d[nt][e][i] * sk[i / 2][0] : fmaf(d[nt][e][i], sk[i / 2][e], sc[nt][bk][i]);
         }
         if (which != (1u << KB) - 1 || key0 + Sh::Step > full_end) {
           // keys that a row does not see; V's scales behind the last key may be
@@ -490,7 +509,7 @@ __global__ void __launch_bounds__(kThreads, (Shape<D, NT>::CtasPerSm)) fa_kv4_fw
             top[nt][c] = fmaxf(sc[nt][0][c], sc[nt][0][2 + c]);
 #pragma unroll
             for (int bk = 1; bk < KB; ++bk) top[nt][c] = fmax3(top[nt][c], sc[nt][bk][c], sc[nt][bk][2 + c]);
-            pass = pass || fmaf(top[nt][c], kUnit, -m[nt][c]) > kLazy;
+            pass = pass || fmaf(top[nt][c], f[nt][c], -m[nt][c]) > kLazy;
           }
         if (__any_sync(0xffffffffu, pass)) {
           float all = v_top;
@@ -507,7 +526,7 @@ __global__ void __launch_bounds__(kThreads, (Shape<D, NT>::CtasPerSm)) fa_kv4_fw
           for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
             for (int c = 0; c < 2; ++c) {
-              const float mx = kUnit * quad_max(top[nt][c]);
+              const float mx = f[nt][c] * quad_max(top[nt][c]);
               float fm = 1.f;
               if (mx - m[nt][c] > kLazy) {
                 fm = ex2_approx(m[nt][c] - mx);
@@ -529,7 +548,7 @@ __global__ void __launch_bounds__(kThreads, (Shape<D, NT>::CtasPerSm)) fa_kv4_fw
           for (int i = 0; i < 2 * KB; ++i) {
             float(&x)[4] = sc[nt][i / 2];
             float x0, x1;
-            f2_unpack(f2_fma(f2_pack(x[2 * (i % 2)], x[2 * (i % 2) + 1]), f2_pack(kUnit, kUnit), neg), x0, x1);
+            f2_unpack(f2_fma(f2_pack(x[2 * (i % 2)], x[2 * (i % 2) + 1]), f2_pack(f[nt][0], f[nt][1]), neg), x0, x1);
             const uint64_t pp = f2_pack(ex2_approx(x0), ex2_approx(x1));
             sum = f2_add(sum, pp);
             f2_unpack(f2_mul(pp, f2_pack(v_up, v_up)), x[2 * (i % 2)], x[2 * (i % 2) + 1]);
@@ -554,23 +573,26 @@ __global__ void __launch_bounds__(kThreads, (Shape<D, NT>::CtasPerSm)) fa_kv4_fw
               vs[half][0] = reinterpret_cast<const uint32_t*>(blk + 8 * D)[2 * (half * 8 + g) + 1];
             }
           }
+          uint32_t b[NT][W][2];
 #pragma unroll
           for (int e = 0; e < W; ++e) {
-            const uint32_t x0 = vw[0][e], x1 = vw[1][e];
-            const uint32_t y0 = __byte_perm(x0, 0, 0x4341), y1 = __byte_perm(x1, 0, 0x4341);
-            const uint32_t z0 = y0 & 0x00f000f0u, z1 = y1 & 0x00f000f0u;
-            const uint32_t a0[4] = {hsub2(x0 & 0x000f000fu, 0x00080008u), hsub2(x0 & 0x00f000f0u, 0x00800080u),
-                                    hsub2(x1 & 0x000f000fu, 0x00080008u), hsub2(x1 & 0x00f000f0u, 0x00800080u)};
-            const uint32_t a1[4] = {hsub2(hsub2(y0, 0x00080008u), z0), hsub2(z0, 0x00800080u),
-                                    hsub2(hsub2(y1, 0x00080008u), z1), hsub2(z1, 0x00800080u)};
             const float s0 = scale_half<BF16>(vs[0][e / 2], e & 1), s1 = scale_half<BF16>(vs[1][e / 2], e & 1);
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt) {
               const float(&pr)[4] = sc[nt][bk];
-              const uint32_t b0 = transpose8x8(pack2<false>(pr[0] * s0, pr[1] * s0));
-              const uint32_t b1 = transpose8x8(pack2<false>(pr[2] * s1, pr[3] * s1));
-              mma16816(o[nt][e][0], a0, b0, b1, o[nt][e][0]);
-              mma16816(o[nt][e][1], a1, b0, b1, o[nt][e][1]);
+              b[nt][e][0] = transpose8x8(pack2<false>(pr[0] * s0, pr[1] * s0));
+              b[nt][e][1] = transpose8x8(pack2<false>(pr[2] * s1, pr[3] * s1));
+            }
+          }
+#pragma unroll
+          for (int e = 0; e < W; ++e) {
+            const uint32_t x0 = vw[0][e], x1 = vw[1][e], y0 = x0 >> 8, y1 = x1 >> 8;
+            const uint32_t a0[4] = {hsub2(x0 & 0x000f000fu, 0x00080008u), hsub2(x0 & 0x00f000f0u, 0x00800080u), hsub2(x1 & 0x000f000fu, 0x00080008u), hsub2(x1 & 0x00f000f0u, 0x00800080u)};
+            const uint32_t a1[4] = {hsub2(y0 & 0x000f000fu, 0x00080008u), hsub2(y0 & 0x00f000f0u, 0x00800080u), hsub2(y1 & 0x000f000fu, 0x00080008u), hsub2(y1 & 0x00f000f0u, 0x00800080u)};
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt) {
+              mma16816(o[nt][e][0], a0, b[nt][e][0], b[nt][e][1], o[nt][e][0]);
+              mma16816(o[nt][e][1], a1, b[nt][e][0], b[nt][e][1], o[nt][e][1]);
             }
           }
         }
@@ -581,10 +603,13 @@ __global__ void __launch_bounds__(kThreads, (Shape<D, NT>::CtasPerSm)) fa_kv4_fw
       slot = slot == ST - 1 ? 0 : slot + 1;
       take = (take + 1) % kBatch;
     }
-    if (!alive) break;
+    if (!alive) {
+      if (begins && p.join_units && lane == 0) p.joins[unit].parts = 0;
+      left = left_then;
+      continue;
+    }
 
     // ---- the unit's result, or this warp's piece of it
-    const bool begins = s0 == 0, ends = s1 == r.steps;
     float* const part = begins && ends ? nullptr : slot_of(p, worker, begins ? 1 : 0, Sh::Slot);
     const float v_down = 1.f / v_up;
 #pragma unroll
@@ -616,12 +641,14 @@ __global__ void __launch_bounds__(kThreads, (Shape<D, NT>::CtasPerSm)) fa_kv4_fw
             p.lse[row0 + row] = (m[nt][c] + log2f(ll)) * 0.69314718055994531f;
         }
       }
-    if (begins && !ends) {
-      join.row = row0;
-      join.rows = rows;
-      join.parts = (int)((r.steps - s1 + each - 1) / each);
+    if (begins) {
+      const Kv4Join mine{row0, rows, (int)worker, (int)((r.steps - s1 + each - 1) / each)};
+      if (p.join_units) {
+        if (lane == 0) p.joins[unit] = mine;
+      } else if (!ends) {
+        join = mine;
+      }
     }
-    at.rem += s1 - s0;
   }
   if (!alive) {
     // copies in flight land before the CTA's shared memory goes
@@ -632,15 +659,16 @@ __global__ void __launch_bounds__(kThreads, (Shape<D, NT>::CtasPerSm)) fa_kv4_fw
     }
     join.parts = 0;
   }
-  if (lane == 0) p.joins[worker] = join;
+  if (lane == 0 && !p.join_units) p.joins[worker] = join;
 }
 
-// O and LSE of the units that lie across workers: one CTA for each worker in
-// which such a unit begins.  Pieces are normalised, with their maximum m (in
-// log2) and sum l beside them; a piece that saw no key has l = 0.
-// Four elements of a row to a thread; threads to spare take the pieces in
-// turn, eight at a time in flight.
-constexpr int kJoinThreads = 512;
+// O and LSE of the units that lie across workers.  Pieces are normalised, with
+// their maximum m (in log2) and sum l beside them; a piece that saw no key has
+// l = 0.  A CTA joins a row, or 128 fours of elements, of a unit; records are
+// kept by unit, or, where units are more than workers, for the unit that
+// begins in a worker and goes on behind it.  Threads to spare take the pieces
+// in turn, eight at a time in flight.
+constexpr int kJoinThreads = 128;
 
 struct Piece {
   float4 o;
@@ -657,19 +685,21 @@ struct Piece {
   }
 };
 
+// It does not let the next kernel start early: an attention kernel's CTAs that
+// settle between this one's CTAs measured slower than ones that wait.
 template <bool BF16, int D, int NT>
 __global__ void __launch_bounds__(kJoinThreads) fa_kv4_join_kernel(const Kv4FwdParams p) {
   using Sh = Shape<D, NT>;
-  static_assert(Sh::Rows * D / 4 <= kJoinThreads, "a thread holds four elements");
   __shared__ Piece shared[kJoinThreads];
   grid_dependency_wait();
-  grid_dependents_launch();
-  const long long worker = blockIdx.x;
-  const Kv4Join j = p.joins[worker];
-  if (j.parts == 0) return;
-  const int items = j.rows * (D / 4), turns = min(kJoinThreads / items, j.parts + 1);
-  const int item = threadIdx.x % items, turn = threadIdx.x / items, row = item / (D / 4), col = 4 * (item % (D / 4));
-  Piece mine{make_float4(0.f, 0.f, 0.f, 0.f), kLeast, 0.f};
+  const Kv4Join j = p.joins[blockIdx.x];
+  const int first = blockIdx.y * p.join_items;
+  if (j.parts == 0 || j.rows * (D / 4) <= first) return;
+  const int worker = j.worker;
+  const int items = min(j.rows * (D / 4) - first, p.join_items), turns = min(kJoinThreads / items, j.parts + 1);
+  const int item = threadIdx.x % items, turn = threadIdx.x / items;
+  const int row = (first + item) / (D / 4), col = 4 * ((first + item) % (D / 4));
+  Piece sum{make_float4(0.f, 0.f, 0.f, 0.f), kLeast, 0.f};
   if (turn < turns) {
     constexpr int kFly = 8;
     for (int k0 = turn; k0 <= j.parts; k0 += kFly * turns) {
@@ -689,26 +719,26 @@ __global__ void __launch_bounds__(kJoinThreads) fa_kv4_join_kernel(const Kv4FwdP
 #pragma unroll
       for (int i = 0; i < kFly; ++i) {
         const float l = ml[i].y;
-        mine.add(make_float4(x[i].x * l, x[i].y * l, x[i].z * l, x[i].w * l), ml[i].x, l);
+        sum.add(make_float4(x[i].x * l, x[i].y * l, x[i].z * l, x[i].w * l), ml[i].x, l);
       }
     }
-    shared[threadIdx.x] = mine;
+    shared[threadIdx.x] = sum;
   }
   __syncthreads();
   if (turn != 0) return;
   for (int k = 1; k < turns; ++k) {
-    const Piece& x = shared[k * items + item];
-    mine.add(x.o, x.m, x.l);
+    const Piece x = shared[k * items + item];
+    sum.add(x.o, x.m, x.l);
   }
-  const float inv = mine.l == 0.f ? 0.f : 1.f / mine.l;
-  const float4 acc = make_float4(mine.o.x * inv, mine.o.y * inv, mine.o.z * inv, mine.o.w * inv);
+  const float inv = sum.l == 0.f ? 0.f : 1.f / sum.l;
+  const float4 acc = make_float4(sum.o.x * inv, sum.o.y * inv, sum.o.z * inv, sum.o.w * inv);
   const long long at = (j.row + row) * D + col;
   if (p.o32)
     *reinterpret_cast<float4*>(static_cast<float*>(p.o) + at) = acc;
   else
     *reinterpret_cast<uint2*>(static_cast<uint16_t*>(p.o) + at) =
         make_uint2(pack2<BF16>(acc.x, acc.y), pack2<BF16>(acc.z, acc.w));
-  if (col == 0) p.lse[j.row + row] = (mine.m + log2f(mine.l)) * 0.69314718055994531f;
+  if (col == 0) p.lse[j.row + row] = (sum.m + log2f(sum.l)) * 0.69314718055994531f;
 }
 
 constexpr int kMaxSms = 160;
@@ -723,13 +753,20 @@ cudaError_t launch(Kv4FwdParams p, void* workspace, int sms, cudaStream_t st) {
   p.row_tiles = (int)((rows + Sh::Rows - 1) / Sh::Rows);
   p.units_per_seq = (long long)p.c.Hkv * p.row_tiles;
   const int grid = (sms < kMaxSms ? sms : kMaxSms) * Sh::CtasPerSm;
+  p.workers = grid * kWarps;
+  const long long units = p.B * p.units_per_seq;
+  p.join_units = units <= p.workers;
+  // a row to a CTA of the joining kernel while that makes few CTAs
+  p.join_items = p.join_units && units * Sh::Rows <= 4096 ? D / 4 : kJoinThreads;
   p.joins = static_cast<Kv4Join*>(workspace);
   p.partials = reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + sizeof(Kv4Join) * kMaxSms * kWarps * 4);
   auto kern = fa_kv4_fwd_kernel<BF16, D, NT>;
   cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)Sh::Smem);
   if (e != cudaSuccess) return e;
   if ((e = launch_chained(kern, dim3(grid), dim3(kThreads), Sh::Smem, st, p)) != cudaSuccess) return e;
-  return launch_chained(fa_kv4_join_kernel<BF16, D, NT>, dim3(grid * kWarps), dim3(kJoinThreads), 0, st, p);
+  const dim3 join_grid(p.join_units ? (unsigned)units : (unsigned)p.workers,
+                       (unsigned)((Sh::Rows * D / 4 + p.join_items - 1) / p.join_items));
+  return launch_chained(fa_kv4_join_kernel<BF16, D, NT>, join_grid, dim3(kJoinThreads), 0, st, p);
 }
 
 }  // namespace
