@@ -199,8 +199,11 @@ def _torch():
 def _stream_handle(stream, device=None) -> Optional[int]:
     """Raw cudaStream_t of ``stream``; None means the current stream of
     ``device`` (the device the call's tensors live on)."""
-    torch = _torch()
     if stream is None:
+        torch = _torch()
+        raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+        if raw is not None and device is not None and device.index is not None:
+            return raw(device.index)   # without a Stream object: 2 us less a call
         stream = torch.cuda.current_stream(device)
     return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
 
@@ -531,20 +534,22 @@ def _check_kv4(pool, page_table, start, count, like, B, Hkv, d):
     n_pages, heads, blocks, width = pool.shape
     if heads != Hkv or width != 18 * d:
         raise ValueError(f"pool holds {heads} heads of {width // 18}, the call has {Hkv} of {d}")
-    if page_table.dim() != 2 or page_table.shape[0] != B:
+    table_shape = page_table.shape
+    if len(table_shape) != 2 or table_shape[0] != B:
         raise ValueError(f"page_table must be [B, max_pages] with B = {B}")
+    int32 = torch.int32
     for name, t in (("page_table", page_table), ("start", start), ("count", count)):
         if t is None and name == "count":
             continue
-        if not t.is_cuda or t.dtype != torch.int32 or not t.is_contiguous():
+        if not t.is_cuda or t.dtype != int32 or not t.is_contiguous():
             raise ValueError(f"{name} must be a contiguous CUDA int32 tensor")
         if t.device != device:
             raise ValueError(f"{name} is on {t.device}, the rows on {device}: they must share a device")
-        if name != "page_table" and (t.dim() != 1 or t.shape[0] != B):
+        if t is not page_table and tuple(t.shape) != (B,):
             raise ValueError(f"{name} must be [B] with B = {B}")
     if pool.device != device:
         raise ValueError(f"pool is on {pool.device}, the rows on {device}: they must share a device")
-    return n_pages, 16 * blocks, page_table.shape[1]
+    return n_pages, 16 * blocks, table_shape[1]
 
 
 def _kv4_call(where, device, stream, fn, *args):
@@ -592,8 +597,8 @@ def fa_kv4_read(pool, page_table, start, count=None, N: Optional[int] = None, k=
         if N is None or dtype not in (torch.bfloat16, torch.float16):
             raise ValueError("without k and v, give N and dtype (bfloat16 or float16)")
         shape = (page_table.shape[0], pool.shape[1], N, pool.shape[3] // 18)
-        k = torch.empty(shape, dtype=dtype, device=pool.device)
-        v = torch.empty(shape, dtype=dtype, device=pool.device)
+        k = pool.new_empty(shape, dtype=dtype)
+        v = torch.empty_like(k)
     _check_bhnd("k", k)
     _check_bhnd("v", v)
     if v.shape != k.shape or v.dtype != k.dtype or v.device != k.device:
@@ -632,11 +637,11 @@ def fa_fwd_kv4(q, pool, page_table, start, count=None, o=None, lse=None, workspa
     if scale is None:
         scale = 1.0 / float(d) ** 0.5
     if o is None:
-        o = torch.empty(q.shape, dtype=torch.float32 if o_fp32 else q.dtype, device=q.device)
+        o = torch.empty_like(q, dtype=torch.float32) if o_fp32 else torch.empty_like(q)
     else:
         _check_bhnd("o", o, q, allow_f32=True)
     if lse is None:
-        lse = torch.empty((B, H, T), dtype=torch.float32, device=q.device)
+        lse = q.new_empty((B, H, T), dtype=torch.float32)
     else:
         _check_lse(lse, q)
     lib = load_library()

@@ -31,9 +31,15 @@ __device__ int g_device_status = 0;
 
 namespace {
 
+// The current device's status word (looked up once per device).
 int* status_ptr() {
-  int* ptr = nullptr;
+  static std::atomic<int*> cache[64];
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return nullptr;
+  int* ptr = cache[dev].load(std::memory_order_relaxed);
+  if (ptr != nullptr) return ptr;
   if (cudaGetSymbolAddress(reinterpret_cast<void**>(&ptr), g_device_status) != cudaSuccess) return nullptr;
+  cache[dev].store(ptr, std::memory_order_relaxed);
   return ptr;
 }
 

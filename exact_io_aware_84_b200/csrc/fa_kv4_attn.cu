@@ -31,6 +31,8 @@
 // 2^8 and P s_V below 2^15.
 #include <cuda_runtime.h>
 
+#include <atomic>
+
 #include "fa.h"
 #include "fa_kernels.h"
 #include "fa_kv4.cuh"
@@ -761,8 +763,16 @@ cudaError_t launch(Kv4FwdParams p, void* workspace, int sms, cudaStream_t st) {
   p.joins = static_cast<Kv4Join*>(workspace);
   p.partials = reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + sizeof(Kv4Join) * kMaxSms * kWarps * 4);
   auto kern = fa_kv4_fwd_kernel<BF16, D, NT>;
-  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)Sh::Smem);
+  static std::atomic<unsigned long long> prepared{0};   // devices on which the kernel may have its shared memory
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
+  const unsigned long long bit = dev < 64 ? 1ull << dev : 0;
+  if ((prepared.load(std::memory_order_relaxed) & bit) == 0) {
+    e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)Sh::Smem);
+    if (e != cudaSuccess) return e;
+    prepared.fetch_or(bit, std::memory_order_relaxed);
+  }
   if ((e = launch_chained(kern, dim3(grid), dim3(kThreads), Sh::Smem, st, p)) != cudaSuccess) return e;
   const dim3 join_grid(p.join_units ? (unsigned)units : (unsigned)p.workers,
                        (unsigned)((Sh::Rows * D / 4 + p.join_items - 1) / p.join_items));
