@@ -9,7 +9,10 @@
 // magnitude, which is clipped to 7s.
 //
 // Both calls stream: a row costs 2D bytes on the 16-bit side and 9D/16 in the
-// cache, and nothing is kept between rows.
+// cache, and nothing is kept between rows.  A warp takes a block of 16
+// positions of a head, lane 4g + t the elements 32e + 8t .. + 7 of the keys g
+// and 8 + g, so that a block's codes are whole 16-byte vectors of its lanes: K
+// as they come out, V after a transposition of half-words (movmatrix).
 #include <cuda_runtime.h>
 
 #include "fa.h"
@@ -42,18 +45,27 @@ __device__ __forceinline__ uint32_t max2_nan(uint32_t a, uint32_t b) {
 
 template <bool BF16>
 __device__ __forceinline__ uint32_t min2_nan(uint32_t a, uint32_t b) {
-  return max2_nan<BF16>(a ^ 0x80008000u, b ^ 0x80008000u) ^ 0x80008000u;
+  uint32_t r;
+  if constexpr (BF16)
+    asm("min.NaN.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+  else
+    asm("min.NaN.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+  return r;
 }
 
-// Largest element (low half) and negative of the smallest (high half) of the
-// 32 elements that four neighbouring lanes hold.
+__device__ __forceinline__ uint32_t transpose8x8(uint32_t x) {
+  uint32_t r;
+  asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(x));
+  return r;
+}
+
+// Largest of a lane's eight elements of a group (low half) and negative of
+// the smallest (high half).
 template <bool BF16>
 __device__ __forceinline__ uint32_t extremes(const uint4& x) {
-  uint32_t hi = max2_nan<BF16>(max2_nan<BF16>(x.x, x.y), max2_nan<BF16>(x.z, x.w));
-  uint32_t lo = min2_nan<BF16>(min2_nan<BF16>(x.x, x.y), min2_nan<BF16>(x.z, x.w)) ^ 0x80008000u;
-  uint32_t v = max2_nan<BF16>(__byte_perm(hi, lo, 0x5410), __byte_perm(hi, lo, 0x7632));
-  v = max2_nan<BF16>(v, __shfl_xor_sync(0xffffffffu, v, 1));
-  return max2_nan<BF16>(v, __shfl_xor_sync(0xffffffffu, v, 2));
+  const uint32_t hi = max2_nan<BF16>(max2_nan<BF16>(x.x, x.y), max2_nan<BF16>(x.z, x.w));
+  const uint32_t lo = min2_nan<BF16>(min2_nan<BF16>(x.x, x.y), min2_nan<BF16>(x.z, x.w)) ^ 0x80008000u;
+  return max2_nan<BF16>(__byte_perm(hi, lo, 0x5410), __byte_perm(hi, lo, 0x7632));
 }
 
 // NaN -> 0, +-inf -> +-largest finite, in both half-words.
@@ -72,22 +84,40 @@ __device__ __forceinline__ uint32_t finite2(uint32_t u) {
   return r;
 }
 
-// Quantises eight elements of a group whose other 24 are in the neighbouring
-// lanes.  Returns the eight codes as a word of two half-words; *s16 gets the
-// group's scale.
+// The extremes of four groups that four neighbouring lanes hold together; lane
+// t gets those of group t.
+template <bool BF16>
+__device__ __forceinline__ uint32_t extremes_of_mine(const uint4 (&x)[4], int t) {
+  uint32_t m[4];
+#pragma unroll
+  for (int j = 0; j < 4; ++j) m[j] = extremes<BF16>(x[j]);
+  const bool up = (t & 2) != 0, odd = (t & 1) != 0;
+  const uint32_t a = max2_nan<BF16>(up ? m[2] : m[0], __shfl_xor_sync(0xffffffffu, up ? m[0] : m[2], 2));
+  const uint32_t b = max2_nan<BF16>(up ? m[3] : m[1], __shfl_xor_sync(0xffffffffu, up ? m[1] : m[3], 2));
+  return max2_nan<BF16>(odd ? b : a, __shfl_xor_sync(0xffffffffu, odd ? a : b, 1));
+}
+
+// Quantises four groups, of each of which four neighbouring lanes hold eight
+// elements: the codes as words of two half-words.  Returns the scale of group
+// t in lane t.
 //
 // x/s is a ratio of two numbers of at most 11 bits, so it lies on k + 1/2
-// exactly or at least 2^-13 away from it; x * (1/s) is within 2^-20 of it (at
-// most 8 in magnitude, two roundings of 2^-24 relative), and adding 2^-16
-// puts ties, and only ties, above the border.
+// exactly or at least 2^-13 away from it; the product with an approximate 1/s
+// is within 2^-19 of it (at most 8 in magnitude).  Adding 2^-16 puts ties, and
+// only ties, above the border.  In sixteenths the sum saturates to [0, 1];
+// times 16 (1 - 2^-22), at most 2^-18 less, and added to 2^23 with truncation,
+// it leaves its floor, 0 to 15, in the low bits.
 template <bool BF16>
-__device__ __forceinline__ uint32_t quantise8(uint4 x, uint16_t* s16) {
+__device__ __forceinline__ uint16_t quantise4(uint4 (&x)[4], uint32_t (&word)[4], int lane) {
   constexpr uint32_t kInf = BF16 ? 0x7f80u : 0x7c00u;
-  uint32_t v = extremes<BF16>(x);
-  const bool odd = (v & 0x7fffu) >= kInf || ((v >> 16) & 0x7fffu) >= kInf;
-  if (__any_sync(0xffffffffu, odd)) {
-    x = make_uint4(finite2<BF16>(x.x), finite2<BF16>(x.y), finite2<BF16>(x.z), finite2<BF16>(x.w));
-    v = extremes<BF16>(x);
+  const int t = lane % 4;
+  uint32_t v = extremes_of_mine<BF16>(x, t);
+  const bool strange = (v & 0x7fffu) >= kInf || ((v >> 16) & 0x7fffu) >= kInf;
+  if (__any_sync(0xffffffffu, strange)) {
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+      x[j] = make_uint4(finite2<BF16>(x[j].x), finite2<BF16>(x[j].y), finite2<BF16>(x[j].z), finite2<BF16>(x[j].w));
+    v = extremes_of_mine<BF16>(x, t);
   }
   const float2 m = unpack2<BF16>(v);
   const float ext = m.x > m.y ? m.x : -m.y;
@@ -96,105 +126,138 @@ __device__ __forceinline__ uint32_t quantise8(uint4 x, uint16_t* s16) {
     h = __bfloat16_as_ushort(__float2bfloat16_rn(ext * -0.125f));
   else
     h = __half_as_ushort(__float2half_rn(ext * -0.125f));
-  float s = kv4_scale<BF16>(h);
-  const bool none = fabsf(s) < 1.17549435e-38f;
-  if (none) h = 0;
-  *s16 = h;
-  const float rs = none ? 0.f : __frcp_rn(s);
-  const uint32_t in[4] = {x.x, x.y, x.z, x.w};
-  uint32_t half[2];
+  const float s = kv4_scale<BF16>(h);
+  float rs;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(rs) : "f"(s));
+  if (fabsf(s) < 1.17549435e-38f) rs = 0.f, h = 0;
+  rs *= 0.0625f;
 #pragma unroll
-  for (int j = 0; j < 2; ++j) {
-    uint32_t c[4];
+  for (int j = 0; j < 4; ++j) {
+    const float r = __shfl_sync(0xffffffffu, rs, (lane & 28) + j);
+    const uint32_t in[4] = {x[j].x, x[j].y, x[j].z, x[j].w};
+    uint32_t half[2];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const float2 f = unpack2<BF16>(in[2 * j + i / 2]);
-      float t = fmaf(i & 1 ? f.y : f.x, rs, 8.5f + 1.f / 65536.f);
-      t = fminf(fmaxf(t, 0.f), 15.5f);
-      c[i] = __float_as_uint(__fadd_rz(t, 8388608.f));   // floor in the low bits
+    for (int i = 0; i < 2; ++i) {
+      uint32_t c[4];
+#pragma unroll
+      for (int k = 0; k < 2; ++k) {
+        const float2 f = unpack2<BF16>(in[2 * i + k]);
+        c[2 * k] = __float_as_uint(__fmaf_rz(__saturatef(fmaf(f.x, r, (8.5f + 1.f / 65536.f) / 16.f)),
+                                             16.f - 1.f / 262144.f, 8388608.f));
+        c[2 * k + 1] = __float_as_uint(__fmaf_rz(__saturatef(fmaf(f.y, r, (8.5f + 1.f / 65536.f) / 16.f)),
+                                                 16.f - 1.f / 262144.f, 8388608.f));
+      }
+      // sum of c_i 16^i; what the 0x4b of each float leaves is above bit 23
+      half[i] = c[0] + c[1] * 16u + c[2] * 256u + c[3] * 4096u;
     }
-    // sum of c_i 16^i; what the 0x4b of each float leaves is above bit 23
-    half[j] = c[0] + (c[1] << 4) + (c[2] << 8) + (c[3] << 12);
+    word[j] = __byte_perm(half[0], half[1], 0x5410);
   }
-  return __byte_perm(half[0], half[1], 0x5410);
+  return h;
+}
+
+// A warp's block of positions: sequence, head, and position of its first key.
+struct Unit {
+  int b, h, n;       // n: tokens of the sequence
+  long long bh, pos, start;
+};
+
+__device__ __forceinline__ Unit unit_of(const Kv4Cache& c, unsigned u, unsigned blocks, int T) {
+  Unit r;
+  r.bh = u / blocks;
+  r.b = (int)r.bh / c.Hkv;
+  r.h = (int)r.bh - r.b * c.Hkv;
+  r.start = c.start[r.b];
+  r.n = kv4_count(c, r.b, T);
+  r.pos = (r.start & ~15ll) + 16ll * (u - (unsigned)r.bh * blocks);
+  return r;
 }
 
 struct WriteParams {
   Kv4Cache c;
   const uint4* k;
   const uint4* v;
-  int B, T;
-  unsigned pairs;       // pairs of neighbouring positions per (sequence, head)
-  long long units;      // B * Hkv * pairs
+  int T;
+  unsigned blocks, units;   // of a head of a sequence, in all
 };
 
-// D/8 lanes hold a row, eight elements each, K and V alike; 2 * D/8 lanes the
-// two tokens of an even position and its successor, whose V codes share words.
 template <bool BF16, int D>
 __global__ void __launch_bounds__(kThreads) fa_kv4_write_kernel(const WriteParams p) {
-  constexpr int L = D / 8, W = D / 32, UPW = 32 / (2 * L);
+  constexpr int W = D / 32;
+  const unsigned u = blockIdx.x * (kThreads / 32) + threadIdx.x / 32;
+  const int lane = threadIdx.x % 32, g = lane / 4, t = lane % 4;
   grid_dependency_wait();
   grid_dependents_launch();
-  const int lane = threadIdx.x % 32, l = lane % L, par = (lane / L) & 1;
-  const long long u = ((long long)blockIdx.x * kThreads + threadIdx.x) / 32 * UPW + lane / (2 * L);
-  uint8_t* blk = nullptr;
-  long long pos = 0;
-  uint4 xk = make_uint4(0, 0, 0, 0), xv = xk;
-  if (u < p.units) {
-    const long long bh = u / p.pairs;
-    const int b = (int)(bh / p.c.Hkv), h = (int)(bh - (long long)b * p.c.Hkv);
-    const int start = p.c.start[b];
-    pos = (start & ~1) + 2ll * (u - bh * p.pairs) + par;
-    const long long t = pos - start;
-    if (t >= 0 && t < kv4_count(p.c, b, p.T)) {
-      blk = kv4_block_of(p.c, b, h, pos, kv4_block_bytes(D));
-      if (blk != nullptr) {
-        const size_t at = ((size_t)bh * p.T + (size_t)t) * L + l;
-        xk = p.k[at];
-        xv = p.v[at];
+  if (u >= p.units) return;
+  const Unit r = unit_of(p.c, u, p.blocks, p.T);
+  const long long first = r.pos - r.start;         // the block's first token, of this call's
+  if (first >= r.n || first <= -16) return;
+  uint8_t* const blk = kv4_block_of(p.c, r.b, r.h, r.pos, kv4_block_bytes(D));
+  if (blk == nullptr) return;
+  auto there = [&](int key) { return first + key >= 0 && first + key < r.n; };
+
+  uint4 x[2][2 * W];   // by half: K's groups, then V's
+#pragma unroll
+  for (int half = 0; half < 2; ++half)
+#pragma unroll
+    for (int j = 0; j < 2 * W; ++j) {
+      x[half][j] = make_uint4(0, 0, 0, 0);
+      if (there(half * 8 + g)) {
+        const uint4* rows = j < W ? p.k : p.v;
+        x[half][j] = rows[((size_t)r.bh * p.T + (size_t)(first + half * 8 + g)) * (D / 8) + 4 * (j % W) + t];
       }
     }
-  }
-  uint16_t sk, sv;
-  const uint32_t wk = quantise8<BF16>(xk, &sk);
-  const uint32_t wv = quantise8<BF16>(xv, &sv);
-  // the even token's lane completes the word of its first four elements of V, the odd one's that of the others
-  const uint32_t other = __shfl_xor_sync(0xffffffffu, par ? wv & 0xffffu : wv >> 16, L);
-  const bool both = __shfl_xor_sync(0xffffffffu, (int)(blk != nullptr), L) != 0 && blk != nullptr;
-  if (blk == nullptr) return;
-  const int key = (int)pos & 15, half = key >> 3;
-  reinterpret_cast<uint32_t*>(blk)[((half * 8 + (key & 7)) * 4 + l % 4) * W + l / 4] = wk;
-  uint32_t* vw = reinterpret_cast<uint32_t*>(blk + 8 * D) + ((half * 8 + l % 4 * 2) * 4 + ((key & 7) >> 1)) * W + l / 4;
-  if (both) {
-    vw[4 * W * par] = par ? __byte_perm(other, wv, 0x7610) : __byte_perm(wv, other, 0x5410);
-  } else {
-    reinterpret_cast<uint16_t*>(vw)[par] = (uint16_t)wv;
-    reinterpret_cast<uint16_t*>(vw + 4 * W)[par] = (uint16_t)(wv >> 16);
-  }
-  if (l % 4 == 0) {
-    uint16_t* s = reinterpret_cast<uint16_t*>(blk + 16 * D) + key * 2 * W + l / 4;
-    s[0] = sk;
-    s[W] = sv;
+#pragma unroll
+  for (int half = 0; half < 2; ++half) {
+    if (first + half * 8 >= r.n || first + half * 8 + 8 <= 0) continue;
+    const bool mine = there(half * 8 + g);
+    uint32_t word[2 * W];
+#pragma unroll
+    for (int q = 0; q < W / 2; ++q) {   // four groups at a time
+      uint4 (&x4)[4] = *reinterpret_cast<uint4(*)[4]>(&x[half][4 * q]);
+      uint32_t (&w4)[4] = *reinterpret_cast<uint32_t(*)[4]>(&word[4 * q]);
+      const uint16_t s = quantise4<BF16>(x4, w4, lane);
+      if (mine) reinterpret_cast<uint16_t*>(blk + 16 * D)[(half * 8 + g) * 2 * W + 4 * q + t] = s;
+    }
+#pragma unroll
+    for (int e = 0; e < W; ++e) word[W + e] = transpose8x8(word[W + e]);   // lane: r = g, keys 2t and 2t + 1
+    uint32_t* const kw = reinterpret_cast<uint32_t*>(blk) + (half * 32 + lane) * W;
+    uint32_t* const vw = reinterpret_cast<uint32_t*>(blk + 8 * D) + (half * 32 + lane) * W;
+    const bool low = there(half * 8 + 2 * t), high = there(half * 8 + 2 * t + 1);
+    if constexpr (W == 4) {
+      if (mine) *reinterpret_cast<uint4*>(kw) = make_uint4(word[0], word[1], word[2], word[3]);
+      if (low && high) *reinterpret_cast<uint4*>(vw) = make_uint4(word[4], word[5], word[6], word[7]);
+    } else {
+      if (mine) *reinterpret_cast<uint2*>(kw) = make_uint2(word[0], word[1]);
+      if (low && high) *reinterpret_cast<uint2*>(vw) = make_uint2(word[2], word[3]);
+    }
+    if (low != high) {   // the other half-words are another call's
+#pragma unroll
+      for (int e = 0; e < W; ++e)
+        reinterpret_cast<uint16_t*>(vw + e)[high] = (uint16_t)(high ? word[W + e] >> 16 : word[W + e]);
+    }
   }
 }
 
-// Eight codes (a word of two half-words) times s, in the 16-bit type.
+// Eight codes (a word of two half-words) times s, rounded once to the 16-bit
+// type: n is exact in it, from 128 + c (bf16) or 1024 + c (fp16).
 template <bool BF16>
-__device__ __forceinline__ uint4 values8(uint32_t w, float s) {
-  uint32_t r[4];
+__device__ __forceinline__ uint4 values8(uint32_t w, uint16_t s) {
+  uint32_t v[4];   // elements i and i + 4
 #pragma unroll
-  for (int j = 0; j < 4; ++j) {
-    const int sh = 16 * (j / 2) + 8 * (j % 2);
-    const float a = (float)((int)((w >> sh) & 15u) - 8) * s, b = (float)((int)((w >> (sh + 4)) & 15u) - 8) * s;
+  for (int i = 0; i < 4; ++i) {
+    const uint32_t c = (w >> (4 * i) & 0x000f000fu) | (BF16 ? 0x43004300u : 0x64006400u);
     if constexpr (BF16) {
-      __nv_bfloat162 h = __floats2bfloat162_rn(a, b);
-      r[j] = *reinterpret_cast<uint32_t*>(&h);
+      const __nv_bfloat162 n = __hsub2(*reinterpret_cast<const __nv_bfloat162*>(&c), __float2bfloat162_rn(136.f));
+      const __nv_bfloat162 y = __hmul2(n, __bfloat162bfloat162(__ushort_as_bfloat16(s)));
+      v[i] = *reinterpret_cast<const uint32_t*>(&y);
     } else {
-      __half2 h = __floats2half2_rn(a, b);
-      r[j] = *reinterpret_cast<uint32_t*>(&h);
+      const __half2 n = __hsub2(*reinterpret_cast<const __half2*>(&c), __float2half2_rn(1032.f));
+      const __half2 y = __hmul2(n, __half2half2(__ushort_as_half(s)));
+      v[i] = *reinterpret_cast<const uint32_t*>(&y);
     }
   }
-  return make_uint4(r[0], r[1], r[2], r[3]);
+  return make_uint4(__byte_perm(v[0], v[1], 0x5410), __byte_perm(v[2], v[3], 0x5410), __byte_perm(v[0], v[1], 0x7632),
+                    __byte_perm(v[2], v[3], 0x7632));
 }
 
 struct ReadParams {
@@ -202,61 +265,91 @@ struct ReadParams {
   uint4* k;
   uint4* v;
   int N;
-  long long rows;       // B * Hkv * N
+  unsigned blocks, units;
 };
 
-// D/8 lanes a row, eight elements each of K and of V.
 template <bool BF16, int D>
 __global__ void __launch_bounds__(kThreads) fa_kv4_read_kernel(const ReadParams p) {
-  constexpr int L = D / 8, W = D / 32;
+  constexpr int W = D / 32;
+  const unsigned u = blockIdx.x * (kThreads / 32) + threadIdx.x / 32;
+  const int lane = threadIdx.x % 32, g = lane / 4, t = lane % 4;
   grid_dependency_wait();
   grid_dependents_launch();
-  const long long i = (long long)blockIdx.x * kThreads + threadIdx.x;
-  const long long row = i / L;
-  const int l = (int)(i % L);
-  if (row >= p.rows) return;
-  const long long bh = row / p.N;
-  const int b = (int)(bh / p.c.Hkv), h = (int)(bh - (long long)b * p.c.Hkv), t = (int)(row - bh * p.N);
-  uint4 xk = make_uint4(0, 0, 0, 0), xv = xk;
-  if (t < kv4_count(p.c, b, p.N)) {
-    const long long pos = (long long)p.c.start[b] + t;
-    const uint8_t* blk = kv4_block_of(p.c, b, h, pos, kv4_block_bytes(D));
+  if (u >= p.units) return;
+  const Unit r = unit_of(p.c, u, p.blocks, p.N);
+  const long long first = r.pos - r.start;
+  if (first >= p.N || first <= -16) return;
+  const uint8_t* blk = nullptr;
+  if (first < r.n) blk = kv4_block_of(p.c, r.b, r.h, r.pos, kv4_block_bytes(D));
+
+  uint32_t kw[2][W], vw[2][W], sw[2][W];   // sw: the scales of a key, two to a word
+#pragma unroll
+  for (int half = 0; half < 2; ++half) {
+#pragma unroll
+    for (int e = 0; e < W; ++e) kw[half][e] = vw[half][e] = sw[half][e] = 0;
     if (blk != nullptr) {
-      const int key = (int)pos & 15, half = key >> 3;
-      const uint16_t* s = reinterpret_cast<const uint16_t*>(blk + 16 * D) + key * 2 * W + l / 4;
-      const uint32_t wk = reinterpret_cast<const uint32_t*>(blk)[((half * 8 + (key & 7)) * 4 + l % 4) * W + l / 4];
-      const uint32_t* vw =
-          reinterpret_cast<const uint32_t*>(blk + 8 * D) + ((half * 8 + l % 4 * 2) * 4 + ((key & 7) >> 1)) * W + l / 4;
-      const uint2 v = make_uint2(vw[0], vw[4 * W]);
-      xk = values8<BF16>(wk, kv4_scale<BF16>(s[0]));
-      xv = values8<BF16>(__byte_perm(v.x, v.y, key & 1 ? 0x7632 : 0x5410), kv4_scale<BF16>(s[W]));
+      if constexpr (W == 4) {
+        const uint4 a = reinterpret_cast<const uint4*>(blk)[half * 32 + lane];
+        const uint4 b = reinterpret_cast<const uint4*>(blk + 8 * D)[half * 32 + lane];
+        const uint4 c = reinterpret_cast<const uint4*>(blk + 16 * D)[half * 8 + g];
+        kw[half][0] = a.x, kw[half][1] = a.y, kw[half][2] = a.z, kw[half][3] = a.w;
+        vw[half][0] = b.x, vw[half][1] = b.y, vw[half][2] = b.z, vw[half][3] = b.w;
+        sw[half][0] = c.x, sw[half][1] = c.y, sw[half][2] = c.z, sw[half][3] = c.w;
+      } else {
+        const uint2 a = reinterpret_cast<const uint2*>(blk)[half * 32 + lane];
+        const uint2 b = reinterpret_cast<const uint2*>(blk + 8 * D)[half * 32 + lane];
+        const uint2 c = reinterpret_cast<const uint2*>(blk + 16 * D)[half * 8 + g];
+        kw[half][0] = a.x, kw[half][1] = a.y;
+        vw[half][0] = b.x, vw[half][1] = b.y;
+        sw[half][0] = c.x, sw[half][1] = c.y;
+      }
     }
   }
-  p.k[(size_t)i] = xk;
-  p.v[(size_t)i] = xv;
+#pragma unroll
+  for (int half = 0; half < 2; ++half) {
+    const long long row = first + half * 8 + g;
+    const bool live = blk != nullptr && row < r.n;
+#pragma unroll
+    for (int e = 0; e < W; ++e) vw[half][e] = transpose8x8(vw[half][e]);
+    if (row < 0 || row >= p.N) continue;
+#pragma unroll
+    for (int e = 0; e < W; ++e) {
+      const size_t at = ((size_t)r.bh * p.N + (size_t)row) * (D / 8) + 4 * e + t;
+      const uint4 none = make_uint4(0, 0, 0, 0);
+      p.k[at] = live ? values8<BF16>(kw[half][e], (uint16_t)(sw[half][e / 2] >> (16 * (e & 1)))) : none;
+      p.v[at] = live ? values8<BF16>(vw[half][e], (uint16_t)(sw[half][(W + e) / 2] >> (16 * (e & 1)))) : none;
+    }
+  }
 }
 
 }  // namespace
 
+// Blocks that T tokens lie in at most, wherever the first one is, and warps.
+static bool units_of(int B, int Hkv, int T, unsigned* blocks, unsigned* units, unsigned* grid) {
+  const long long a = ((long long)T + 14) / 16 + 1, all = a * B * Hkv;
+  *blocks = (unsigned)a;
+  *units = (unsigned)all;
+  *grid = (unsigned)((all + kThreads / 32 - 1) / (kThreads / 32));
+  return all < (1ll << 32) - kThreads;
+}
+
 cudaError_t launch_kv4_write(bool bf16, int d, const Kv4Cache& c, const void* k, const void* v, int B, int T,
                              cudaStream_t st) {
-  WriteParams p{c, static_cast<const uint4*>(k), static_cast<const uint4*>(v), B, T, (unsigned)(T / 2 + 1), 0};
-  p.units = (long long)B * c.Hkv * p.pairs;
-  const long long per_cta = kThreads / 32 * (32 / (2 * (d / 8)));
-  const long long grid = (p.units + per_cta - 1) / per_cta;
-  if (grid > 0x7fffffffll) return cudaErrorInvalidConfiguration;
+  WriteParams p{c, static_cast<const uint4*>(k), static_cast<const uint4*>(v), T, 0, 0};
+  unsigned grid;
+  if (!units_of(B, c.Hkv, T, &p.blocks, &p.units, &grid)) return cudaErrorInvalidConfiguration;
   auto kern = bf16 ? (d == 64 ? fa_kv4_write_kernel<true, 64> : fa_kv4_write_kernel<true, 128>)
                    : (d == 64 ? fa_kv4_write_kernel<false, 64> : fa_kv4_write_kernel<false, 128>);
-  return launch_chained(kern, dim3((unsigned)grid), dim3(kThreads), 0, st, p);
+  return launch_chained(kern, dim3(grid), dim3(kThreads), 0, st, p);
 }
 
 cudaError_t launch_kv4_read(bool bf16, int d, const Kv4Cache& c, void* k, void* v, int B, int N, cudaStream_t st) {
-  ReadParams p{c, static_cast<uint4*>(k), static_cast<uint4*>(v), N, (long long)B * c.Hkv * N};
-  const long long grid = (p.rows * (d / 8) + kThreads - 1) / kThreads;
-  if (grid > 0x7fffffffll) return cudaErrorInvalidConfiguration;
+  ReadParams p{c, static_cast<uint4*>(k), static_cast<uint4*>(v), N, 0, 0};
+  unsigned grid;
+  if (!units_of(B, c.Hkv, N, &p.blocks, &p.units, &grid)) return cudaErrorInvalidConfiguration;
   auto kern = bf16 ? (d == 64 ? fa_kv4_read_kernel<true, 64> : fa_kv4_read_kernel<true, 128>)
                    : (d == 64 ? fa_kv4_read_kernel<false, 64> : fa_kv4_read_kernel<false, 128>);
-  return launch_chained(kern, dim3((unsigned)grid), dim3(kThreads), 0, st, p);
+  return launch_chained(kern, dim3(grid), dim3(kThreads), 0, st, p);
 }
 
 }  // namespace fa
