@@ -32,6 +32,27 @@ inline cudaError_t launch_chained(void (*kern)(Params...), dim3 grid, dim3 block
   return cudaLaunchKernelEx(&cfg, kern, std::forward<Args>(args)...);
 }
 
+// The same in clusters of `cluster` CTAs.
+template <typename... Params, typename... Args>
+inline cudaError_t launch_chained_clusters(void (*kern)(Params...), dim3 grid, dim3 block, size_t smem,
+                                           cudaStream_t st, int cluster, Args&&... args) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = grid;
+  cfg.blockDim = block;
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = st;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = (unsigned)cluster;
+  attr[1].val.clusterDim.y = 1;
+  attr[1].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 2;
+  return cudaLaunchKernelEx(&cfg, kern, std::forward<Args>(args)...);
+}
+
 constexpr int kBlockM = 128;  // query rows per Q tile (tcgen05 M)
 constexpr int kBlockN = 128;  // keys per K/V tile
 
@@ -159,7 +180,8 @@ struct Kv4FwdParams {
   // set by the launch
   int row_tiles;             // tiles of query rows a key head
   long long units_per_seq;   // Hkv * row_tiles
-  int workers;               // warps of the grid
+  int cluster;               // CTAs that share a unit, where clusters do
+  int workers;               // warps of the grid, where they do not
   int join_units;            // joins go by unit, else by worker
   int join_items;            // fours of elements a CTA of the joining kernel
   Kv4Join* joins;            // [units or workers]

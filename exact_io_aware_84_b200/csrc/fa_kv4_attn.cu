@@ -160,7 +160,80 @@ __device__ __forceinline__ float* slot_of(const Kv4FwdParams& p, long long worke
   return p.partials + (size_t)(2 * worker + which) * slot_floats;
 }
 
+// Part of a row's result: O weighted by l, the maximum m (in log2) and sum l.
+struct Piece {
+  float4 o;
+  float m, l;
+
+  // The two as one; o stays a sum weighted by l.
+  __device__ __forceinline__ void add(const float4& x, float xm, float xl) {
+    const float top = fmaxf(m, xm);
+    const float fa = ex2_approx(m - top), fb = ex2_approx(xm - top);
+    o.x = o.x * fa + x.x * fb, o.y = o.y * fa + x.y * fb;
+    o.z = o.z * fa + x.z * fb, o.w = o.w * fa + x.w * fb;
+    l = l * fa + xl * fb;
+    m = top;
+  }
+};
+
+template <bool BF16>
+__device__ __forceinline__ void store_result(const Kv4FwdParams& p, const Piece& x, long long row, int D, int col) {
+  const float inv = x.l == 0.f ? 0.f : 1.f / x.l;
+  const float4 o = make_float4(x.o.x * inv, x.o.y * inv, x.o.z * inv, x.o.w * inv);
+  if (p.o32)
+    *reinterpret_cast<float4*>(static_cast<float*>(p.o) + row * D + col) = o;
+  else
+    *reinterpret_cast<uint2*>(static_cast<uint16_t*>(p.o) + row * D + col) =
+        make_uint2(pack2<BF16>(o.x, o.y), pack2<BF16>(o.z, o.w));
+  if (col == 0) p.lse[row] = (x.m + log2f(x.l)) * 0.69314718055994531f;
+}
+
+__device__ __forceinline__ void cluster_sync() {
+  asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+
+// Joins the pieces that the warps of a cluster have left at the start of their
+// rings: the CTAs divide the unit's rows and columns.
 template <bool BF16, int D, int NT>
+__device__ __forceinline__ void join_in_cluster(const Kv4FwdParams& p, const uint8_t* ring_all) {
+  using Sh = Shape<D, NT>;
+  __syncwarp();
+  cluster_sync();
+  const unsigned unit = blockIdx.x / (unsigned)p.cluster, rank = blockIdx.x % (unsigned)p.cluster;
+  const unsigned u = unit % (unsigned)p.units_per_seq, tile = u % (unsigned)p.row_tiles;
+  const long long group_rows = (long long)(p.H / p.c.Hkv) * p.T;
+  const long long row0 = (unit / (unsigned)p.units_per_seq * (long long)p.c.Hkv + u / p.row_tiles) * group_rows + (long long)tile * Sh::Rows;
+  const long long left = group_rows - (long long)tile * Sh::Rows;
+  const int rows = left < Sh::Rows ? (int)left : Sh::Rows;
+  const uint32_t base = smem_u32(ring_all);
+  for (int i = rank * kThreads + threadIdx.x; i < rows * (D / 4); i += p.cluster * kThreads) {
+    const int row = i / (D / 4), col = 4 * (i % (D / 4));
+    Piece sum{make_float4(0.f, 0.f, 0.f, 0.f), kLeast, 0.f};
+#pragma unroll 2
+    for (int r = 0; r < p.cluster; ++r) {
+      uint32_t there;
+      asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(there) : "r"(base), "r"(r));
+#pragma unroll
+      for (int w = 0; w < kWarps; ++w) {
+        const uint32_t at = there + w * Sh::Stages * Sh::Stage;
+        float4 x;
+        float m, l;
+        asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
+                     : "=f"(x.x), "=f"(x.y), "=f"(x.z), "=f"(x.w)
+                     : "r"(at + (row * D + col) * 4));
+        asm volatile("ld.shared::cluster.v2.f32 {%0, %1}, [%2];" : "=f"(m), "=f"(l) : "r"(at + (Sh::Rows * D + 2 * row) * 4));
+        sum.add(make_float4(x.x * l, x.y * l, x.z * l, x.w * l), m, l);
+      }
+    }
+    store_result<BF16>(p, sum, row0 + row, D, col);
+  }
+  __syncwarp();
+  cluster_sync();   // no CTA ends while another reads its shared memory
+}
+
+// Near: a cluster of CTAs to a unit, whose warps divide its steps and whose
+// shared memory joins them.  Else all warps divide all steps.
+template <bool BF16, int D, int NT, bool Near>
 __global__ void __launch_bounds__(kThreads, (Shape<D, NT>::CtasPerSm)) fa_kv4_fwd_kernel(const Kv4FwdParams p) {
   using Sh = Shape<D, NT>;
   constexpr int W = Sh::W, ST = Sh::Stages, KB = Sh::Blocks, Block = Sh::Block;
@@ -179,56 +252,9 @@ __global__ void __launch_bounds__(kThreads, (Shape<D, NT>::CtasPerSm)) fa_kv4_fw
   if (threadIdx.x == 0) abort_flag = 0;
   if (lane < ST) mbar_init(bar0 + 8 * lane, KB);
   fence_mbar_init();
+  __syncthreads();
   grid_dependency_wait();
   grid_dependents_launch();
-
-  // ---- how many steps there are, and which of them are this warp's
-  const int per = (p.B + kThreads - 1) / kThreads;
-  long long mine = 0;
-  for (int i = 0, b = threadIdx.x * per; i < per && b < p.B; ++i, ++b) {
-    const Reach r(p, p.c.start[b], kv4_count(p.c, b, p.T), Sh::Step);
-    mine += r.steps;
-    if (blockIdx.x == 0 && r.n > 0 && r.start + r.n > r.keys && r.start + r.n > 0)   // past the page table
-      atomicCAS(p.c.status, 0, FA_ERR_PAGE);
-  }
-  mine *= p.units_per_seq;
-  long long incl = mine;
-#pragma unroll
-  for (int d = 1; d < 32; d *= 2) {
-    const long long o = __shfl_up_sync(0xffffffffu, incl, d);
-    if (lane >= d) incl += o;
-  }
-  if (lane == 31) warp_sum[warp] = incl;
-  __syncthreads();
-  long long before = 0, total = 0;
-#pragma unroll
-  for (int i = 0; i < kWarps; ++i) {
-    if (i < warp) before += warp_sum[i];
-    total += warp_sum[i];
-  }
-  chunk_sum[threadIdx.x] = before + incl - mine;
-  __syncthreads();
-
-  const long long workers = p.workers, worker = (long long)blockIdx.x * kWarps + warp;
-  const long long each = (total + workers - 1) / workers;
-  const long long lo = worker * each, hi = lo + each < total ? lo + each : total;
-  // the last chunk of sequences that does not begin behind a step
-  auto chunk_of = [&](long long step) {
-    int n = 0;
-#pragma unroll
-    for (int i = 0; i < kThreads / 32; ++i) n += __popc(__ballot_sync(0xffffffffu, chunk_sum[32 * i + lane] <= step));
-    return n - 1;
-  };
-  const int first = chunk_of(lo), b_seen = chunk_of(lo - warp * each) * per;
-  const long long first_sum = chunk_sum[first];
-  for (int i = threadIdx.x; i < kSeen && b_seen + i < p.B; i += kThreads)
-    seen[i] = make_int2(p.c.start[b_seen + i], kv4_count(p.c, b_seen + i, p.T));
-  __syncthreads();
-  if (lo >= hi) {
-    if (lane == 0 && !p.join_units) p.joins[worker].parts = 0;
-    return;
-  }
-  int left = (int)(hi - lo);   // steps (2^31 of them would be hours)
 
   // A position in the sequence of all steps: `rem` steps behind the first one
   // of sequence b.  settle moves it on to the sequence that it lies in.
@@ -236,13 +262,15 @@ __global__ void __launch_bounds__(kThreads, (Shape<D, NT>::CtasPerSm)) fa_kv4_fw
     int b;
     long long rem;
   };
+  int b_seen = 0;
   auto reach = [&](int b) {
     const int i = b - b_seen;
-    const int2 x = i < kSeen ? seen[i] : make_int2(p.c.start[b], kv4_count(p.c, b, p.T));
+    const int2 x = !Near && i < kSeen ? seen[i] : make_int2(p.c.start[b], kv4_count(p.c, b, p.T));
     return Reach(p, x.x, x.y, Sh::Step);
   };
   auto settle = [&](Cursor& c) {
     Reach r = reach(c.b);
+    if constexpr (Near) return r;
     while (c.rem >= (long long)r.steps * p.units_per_seq) {
       if (c.b == p.B - 1) break;   // behind the last step
       c.rem -= (long long)r.steps * p.units_per_seq;
@@ -250,8 +278,73 @@ __global__ void __launch_bounds__(kThreads, (Shape<D, NT>::CtasPerSm)) fa_kv4_fw
     }
     return r;
   };
-  Cursor at{first * per, lo - first_sum};
-  settle(at);
+  auto past_table = [&](const Reach& r) {
+    if (r.n > 0 && r.start + r.n > r.keys && r.start + r.n > 0) atomicCAS(p.c.status, 0, FA_ERR_PAGE);
+  };
+
+  // ---- which steps are this warp's
+  const long long worker = (long long)blockIdx.x * kWarps + warp;
+  long long each = 0;
+  int left = 0;   // steps (2^31 of them would be hours)
+  Cursor at{0, 0};
+  if constexpr (Near) {
+    const unsigned unit = blockIdx.x / (unsigned)p.cluster, u = unit % (unsigned)p.units_per_seq;
+    at.b = (int)(unit / (unsigned)p.units_per_seq);
+    const Reach r = reach(at.b);
+    if (u == 0 && threadIdx.x == 0) past_table(r);
+    const long long part = worker - (long long)unit * p.cluster * kWarps, parts = p.cluster * kWarps;
+    const int s0 = (int)(part * r.steps / parts);
+    left = (int)((part + 1) * r.steps / parts) - s0;
+    at.rem = (long long)u * r.steps + s0;
+  } else {
+    const int per = (p.B + kThreads - 1) / kThreads;
+    long long mine = 0;
+    for (int i = 0, b = threadIdx.x * per; i < per && b < p.B; ++i, ++b) {
+      const Reach r(p, p.c.start[b], kv4_count(p.c, b, p.T), Sh::Step);
+      mine += r.steps;
+      if (blockIdx.x == 0) past_table(r);
+    }
+    mine *= p.units_per_seq;
+    long long incl = mine;
+#pragma unroll
+    for (int d = 1; d < 32; d *= 2) {
+      const long long o = __shfl_up_sync(0xffffffffu, incl, d);
+      if (lane >= d) incl += o;
+    }
+    if (lane == 31) warp_sum[warp] = incl;
+    __syncthreads();
+    long long before = 0, total = 0;
+#pragma unroll
+    for (int i = 0; i < kWarps; ++i) {
+      if (i < warp) before += warp_sum[i];
+      total += warp_sum[i];
+    }
+    chunk_sum[threadIdx.x] = before + incl - mine;
+    __syncthreads();
+
+    each = (total + p.workers - 1) / p.workers;
+    const long long lo = worker * each, hi = lo + each < total ? lo + each : total;
+    // the last chunk of sequences that does not begin behind a step
+    auto chunk_of = [&](long long step) {
+      int n = 0;
+#pragma unroll
+      for (int i = 0; i < kThreads / 32; ++i) n += __popc(__ballot_sync(0xffffffffu, chunk_sum[32 * i + lane] <= step));
+      return n - 1;
+    };
+    const int first = chunk_of(lo);
+    b_seen = chunk_of(lo - warp * each) * per;
+    const long long first_sum = chunk_sum[first];
+    for (int i = threadIdx.x; i < kSeen && b_seen + i < p.B; i += kThreads)
+      seen[i] = make_int2(p.c.start[b_seen + i], kv4_count(p.c, b_seen + i, p.T));
+    __syncthreads();
+    if (lo >= hi) {
+      if (lane == 0 && !p.join_units) p.joins[worker].parts = 0;
+      return;
+    }
+    left = (int)(hi - lo);
+    at = Cursor{first * per, lo - first_sum};
+    settle(at);
+  }
 
   // ---- the producer: lane i looks up block i % KB of step kBatch k + i / KB
   const int my_step = lane / KB;
@@ -297,6 +390,7 @@ __global__ void __launch_bounds__(kThreads, (Shape<D, NT>::CtasPerSm)) fa_kv4_fw
   for (int i = 0; i < ST; ++i)
     if (i < left) produce(i, i, i);
 
+  const bool no_steps = left == 0;
   const WaitCtx wc{p.wait_limit_ns, &abort_flag, p.c.status};
   Kv4Join join{0, 0, 0, 0};
   const int group = p.H / p.c.Hkv;
@@ -322,7 +416,7 @@ __global__ void __launch_bounds__(kThreads, (Shape<D, NT>::CtasPerSm)) fa_kv4_fw
     const long long unit = (long long)at.b * p.units_per_seq + u;
     at.rem += s1 - s0;
     if (!alive) {   // a wait ran out before: nothing to join
-      if (begins && p.join_units && lane == 0) p.joins[unit].parts = 0;
+      if (!Near && begins && p.join_units && lane == 0) p.joins[unit].parts = 0;
       left = left_then;
       continue;
     }
@@ -606,13 +700,14 @@ __global__ void __launch_bounds__(kThreads, (Shape<D, NT>::CtasPerSm)) fa_kv4_fw
       take = (take + 1) % kBatch;
     }
     if (!alive) {
-      if (begins && p.join_units && lane == 0) p.joins[unit].parts = 0;
+      if (!Near && begins && p.join_units && lane == 0) p.joins[unit].parts = 0;
       left = left_then;
       continue;
     }
 
     // ---- the unit's result, or this warp's piece of it
-    float* const part = begins && ends ? nullptr : slot_of(p, worker, begins ? 1 : 0, Sh::Slot);
+    float* part = begins && ends ? nullptr : slot_of(p, worker, begins ? 1 : 0, Sh::Slot);
+    if constexpr (Near) part = reinterpret_cast<float*>(ring);
     const float v_down = 1.f / v_up;
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt)
@@ -643,7 +738,7 @@ __global__ void __launch_bounds__(kThreads, (Shape<D, NT>::CtasPerSm)) fa_kv4_fw
             p.lse[row0 + row] = (m[nt][c] + log2f(ll)) * 0.69314718055994531f;
         }
       }
-    if (begins) {
+    if (!Near && begins) {
       const Kv4Join mine{row0, rows, (int)worker, (int)((r.steps - s1 + each - 1) / each)};
       if (p.join_units) {
         if (lane == 0) p.joins[unit] = mine;
@@ -661,7 +756,16 @@ __global__ void __launch_bounds__(kThreads, (Shape<D, NT>::CtasPerSm)) fa_kv4_fw
     }
     join.parts = 0;
   }
-  if (lane == 0 && !p.join_units) p.joins[worker] = join;
+  if (!Near && lane == 0 && !p.join_units) p.joins[worker] = join;
+  if constexpr (Near) {
+    if (no_steps || !alive) {   // an empty piece
+      float* const part = reinterpret_cast<float*>(ring);
+      for (int i = lane; i < Sh::Rows * D; i += 32) part[i] = 0.f;
+      for (int i = lane; i < Sh::Rows; i += 32)
+        *reinterpret_cast<float2*>(part + Sh::Rows * D + 2 * i) = make_float2(kLeast, 0.f);
+    }
+    join_in_cluster<BF16, D, NT>(p, ring_all);
+  }
 }
 
 // O and LSE of the units that lie across workers.  Pieces are normalised, with
@@ -671,21 +775,6 @@ __global__ void __launch_bounds__(kThreads, (Shape<D, NT>::CtasPerSm)) fa_kv4_fw
 // begins in a worker and goes on behind it.  Threads to spare take the pieces
 // in turn, eight at a time in flight.
 constexpr int kJoinThreads = 128;
-
-struct Piece {
-  float4 o;
-  float m, l;
-
-  // The two as one; o stays a sum weighted by l.
-  __device__ __forceinline__ void add(const float4& x, float xm, float xl) {
-    const float top = fmaxf(m, xm);
-    const float fa = ex2_approx(m - top), fb = ex2_approx(xm - top);
-    o.x = o.x * fa + x.x * fb, o.y = o.y * fa + x.y * fb;
-    o.z = o.z * fa + x.z * fb, o.w = o.w * fa + x.w * fb;
-    l = l * fa + xl * fb;
-    m = top;
-  }
-};
 
 // It does not let the next kernel start early: an attention kernel's CTAs that
 // settle between this one's CTAs measured slower than ones that wait.
@@ -732,47 +821,59 @@ __global__ void __launch_bounds__(kJoinThreads) fa_kv4_join_kernel(const Kv4FwdP
     const Piece x = shared[k * items + item];
     sum.add(x.o, x.m, x.l);
   }
-  const float inv = sum.l == 0.f ? 0.f : 1.f / sum.l;
-  const float4 acc = make_float4(sum.o.x * inv, sum.o.y * inv, sum.o.z * inv, sum.o.w * inv);
-  const long long at = (j.row + row) * D + col;
-  if (p.o32)
-    *reinterpret_cast<float4*>(static_cast<float*>(p.o) + at) = acc;
-  else
-    *reinterpret_cast<uint2*>(static_cast<uint16_t*>(p.o) + at) =
-        make_uint2(pack2<BF16>(acc.x, acc.y), pack2<BF16>(acc.z, acc.w));
-  if (col == 0) p.lse[j.row + row] = (sum.m + log2f(sum.l)) * 0.69314718055994531f;
+  store_result<BF16>(p, sum, j.row + row, D, col);
 }
 
 constexpr int kMaxSms = 160;
+constexpr int kNear = 8;
 
 // Query rows of a unit, in tiles of 8: what K's and V's decoding is shared by.
 int row_tiles_of(int d, long long rows) { return rows <= 8 ? 1 : rows <= 16 || d == 128 ? 2 : 4; }
 
+// Lets a kernel have its dynamic shared memory, once per device.
+template <typename Kernel>
+cudaError_t prepare(Kernel* kern, size_t smem, std::atomic<unsigned long long>* done) {
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  const unsigned long long bit = dev < 64 ? 1ull << dev : 0;
+  if ((done->load(std::memory_order_relaxed) & bit) != 0) return cudaSuccess;
+  e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+  if (e == cudaSuccess) done->fetch_or(bit, std::memory_order_relaxed);
+  return e;
+}
+
 template <bool BF16, int D, int NT>
 cudaError_t launch(Kv4FwdParams p, void* workspace, int sms, cudaStream_t st) {
   using Sh = Shape<D, NT>;
+  static std::atomic<unsigned long long> near_done{0}, far_done{0};
+  cudaError_t e;
   const long long rows = (long long)(p.H / p.c.Hkv) * p.T;
   p.row_tiles = (int)((rows + Sh::Rows - 1) / Sh::Rows);
   p.units_per_seq = (long long)p.c.Hkv * p.row_tiles;
+  const long long units = p.B * p.units_per_seq;
+
+  // Few and short units: a cluster each.  The largest cluster that finds room at
+  // once and has a step for each warp, while no warp gets more than kNear.
+  const long long most = (((long long)p.c.max_pages << p.c.page_shift) + Sh::Step - 1) / Sh::Step;   // steps of a unit
+  int cluster = 8;
+  while (cluster > 1 && (units * cluster > (long long)sms * Sh::CtasPerSm || cluster / 2 * kWarps >= most)) cluster /= 2;
+  if (units * cluster <= (long long)sms * Sh::CtasPerSm && most <= (long long)cluster * kWarps * kNear) {
+    p.cluster = cluster;
+    auto kern = fa_kv4_fwd_kernel<BF16, D, NT, true>;
+    if ((e = prepare(kern, Sh::Smem, &near_done)) != cudaSuccess) return e;
+    return launch_chained_clusters(kern, dim3((unsigned)(units * cluster)), dim3(kThreads), Sh::Smem, st, cluster, p);
+  }
+
   const int grid = (sms < kMaxSms ? sms : kMaxSms) * Sh::CtasPerSm;
   p.workers = grid * kWarps;
-  const long long units = p.B * p.units_per_seq;
   p.join_units = units <= p.workers;
   // a row to a CTA of the joining kernel while that makes few CTAs
   p.join_items = p.join_units && units * Sh::Rows <= 4096 ? D / 4 : kJoinThreads;
   p.joins = static_cast<Kv4Join*>(workspace);
   p.partials = reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + sizeof(Kv4Join) * kMaxSms * kWarps * 4);
-  auto kern = fa_kv4_fwd_kernel<BF16, D, NT>;
-  static std::atomic<unsigned long long> prepared{0};   // devices on which the kernel may have its shared memory
-  int dev = 0;
-  cudaError_t e = cudaGetDevice(&dev);
-  if (e != cudaSuccess) return e;
-  const unsigned long long bit = dev < 64 ? 1ull << dev : 0;
-  if ((prepared.load(std::memory_order_relaxed) & bit) == 0) {
-    e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)Sh::Smem);
-    if (e != cudaSuccess) return e;
-    prepared.fetch_or(bit, std::memory_order_relaxed);
-  }
+  auto kern = fa_kv4_fwd_kernel<BF16, D, NT, false>;
+  if ((e = prepare(kern, Sh::Smem, &far_done)) != cudaSuccess) return e;
   if ((e = launch_chained(kern, dim3(grid), dim3(kThreads), Sh::Smem, st, p)) != cudaSuccess) return e;
   const dim3 join_grid(p.join_units ? (unsigned)units : (unsigned)p.workers,
                        (unsigned)((Sh::Rows * D / 4 + p.join_items - 1) / p.join_items));

@@ -401,6 +401,103 @@ def test_a_cache_past_four_gigabytes():
     _ok()
 
 
+# A table with room for 2^17 positions: the attention then cannot count on short sequences, and divides
+# all of them over the whole grid; with a tight one, few and short sequences get a cluster of CTAs each.
+
+
+def _room(c, positions=1 << 17):
+    wide = torch.full((c.B, positions // c.page), -7, dtype=torch.int32, device="cuda")
+    wide[:, : c.table.shape[1]] = c.table
+    c.table = wide.contiguous()
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp16"])
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("H,Hkv", [(2, 2), (8, 1), (12, 4), (5, 1), (33, 1)])
+@pytest.mark.parametrize("T,causal", [(1, True), (3, True), (3, False)])
+def test_room_for_long_sequences(T, causal, H, Hkv, d, dtype):
+    start = [0, 14, 900]
+    c = Cache(3, Hkv, d, dtype, 32, 910, seed=H + Hkv + d + T)
+    c.write([0] * 3, 910)
+    _room(c)
+    c.check_attention(_rows(c.g, dtype, 3, H, T, d), start, causal=causal)
+    _ok()
+
+
+@pytest.mark.parametrize("length", [1, 16, 63, 64, 65, 127, 129, 1023, 2049, 5000])
+def test_room_and_lengths(length):
+    c = Cache(2, 2, 128, "bf16", 16, length, seed=length)
+    c.write([0, 0], length)
+    _room(c)
+    c.check_attention(_rows(c.g, "bf16", 2, 8, 1, 128), [length - 1, length // 2])
+    _ok()
+
+
+@pytest.mark.parametrize("T", [2, 16, 40, 100])
+@pytest.mark.parametrize("d", [64, 128])
+def test_room_and_several_new_tokens(T, d):
+    c = Cache(3, 2, d, "fp16", 16, T + 130, seed=T)
+    start, count = [0, 129, 57], [T, T, (T + 1) // 2]
+    c.write([0] * 3, T + 130)
+    _room(c)
+    for causal in (False, True):
+        c.check_attention(_rows(c.g, "fp16", 3, 6, T, d), start, count=count, causal=causal)
+    _ok()
+
+
+@pytest.mark.parametrize("wide", [False, True])
+def test_more_units_than_warps(wide):
+    """2400 key heads of short sequences, some of them empty."""
+    B = 1200
+    c = Cache(B, 2, 64, "bf16", 64, 64, seed=27)
+    c.write([0] * B, 64)
+    if wide:
+        _room(c, 1 << 12)
+    count = [0 if b % 11 == 3 else 1 for b in range(B)]
+    c.check_attention(_rows(c.g, "bf16", B, 2, 1, 64), [(b * 7) % 64 for b in range(B)], count=count)
+    _ok()
+
+
+def test_room_and_rows_that_see_no_key():
+    c = Cache(5, 1, 64, "bf16", 16, 40, seed=11)
+    c.write([0] * 5, 40)
+    _room(c)
+    q = _rows(c.g, "bf16", 5, 3, 4, 64)
+    c.check_attention(q, [10, 10, 0, 36, 0], count=[0, -4, 1, 4, 99])
+    for causal in (True, False):
+        c.check_attention(q, [-2, -4, -50, 5, -3], causal=causal)
+    _ok()
+
+
+def test_room_and_missing_pages():
+    c = Cache(2, 2, 64, "bf16", 16, 640, seed=28)
+    c.write([0, 0], 640)
+    _room(c)
+    c.table[0, 3], c.table[1, 20] = c.pool.shape[0], -1
+    missing = np.zeros((2, 640), bool)
+    missing[0, 48:64] = missing[1, 320:336] = True
+    for x in (c.k, c.v):
+        x[np.broadcast_to(missing[:, None, :, None], x.shape)] = 0
+    c.check_attention(_rows(c.g, "bf16", 2, 4, 2, 64), [638, 600], missing=missing)
+    assert fa.fa_last_device_status() == fa.FA_ERR_PAGE
+
+
+@pytest.mark.parametrize("wide", [False, True])
+def test_one_channel_far_above_the_others(wide):
+    """q enters relative to its row's largest element, and P s_V relative to the largest scale."""
+    c = Cache(2, 1, 128, "bf16", 16, 700, seed=29)
+    k, v = _rows(c.g, "bf16", 2, 1, 700, 128), _rows(c.g, "bf16", 2, 1, 700, 128)
+    k[..., 5] *= 2.0**-12
+    v[..., 70] *= 2.0**12
+    c.write([0, 0], 700, k=k, v=v)
+    if wide:
+        _room(c)
+    q = _rows(c.g, "bf16", 2, 8, 1, 128)
+    q[..., 5] *= 2.0**12
+    c.check_attention(q, [699, 350])
+    _ok()
+
+
 # ---------------------------------------------------------------- streams, graphs, use
 
 
