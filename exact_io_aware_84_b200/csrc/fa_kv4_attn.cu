@@ -150,12 +150,6 @@ struct Reach {
   }
 };
 
-// Which of the sequence's units a position lies in.
-__device__ __forceinline__ unsigned unit_at(long long rem, int steps) {
-  if (rem >> 32 == 0) return (unsigned)rem / (unsigned)steps;
-  return (unsigned)((unsigned long long)rem / (unsigned)steps);
-}
-
 __device__ __forceinline__ float* slot_of(const Kv4FwdParams& p, long long worker, int which, int slot_floats) {
   return p.partials + (size_t)(2 * worker + which) * slot_floats;
 }
@@ -256,11 +250,9 @@ __global__ void __launch_bounds__(kThreads, (Shape<D, NT>::CtasPerSm)) fa_kv4_fw
   grid_dependency_wait();
   grid_dependents_launch();
 
-  // A position in the sequence of all steps: `rem` steps behind the first one
-  // of sequence b.  settle moves it on to the sequence that it lies in.
-  struct Cursor {
-    int b;
-    long long rem;
+  // A unit: sequence, key head, tile of query rows.
+  struct Place {
+    int b, h, tile;
   };
   int b_seen = 0;
   auto reach = [&](int b) {
@@ -268,15 +260,13 @@ __global__ void __launch_bounds__(kThreads, (Shape<D, NT>::CtasPerSm)) fa_kv4_fw
     const int2 x = !Near && i < kSeen ? seen[i] : make_int2(p.c.start[b], kv4_count(p.c, b, p.T));
     return Reach(p, x.x, x.y, Sh::Step);
   };
-  auto settle = [&](Cursor& c) {
-    Reach r = reach(c.b);
-    if constexpr (Near) return r;
-    while (c.rem >= (long long)r.steps * p.units_per_seq) {
-      if (c.b == p.B - 1) break;   // behind the last step
-      c.rem -= (long long)r.steps * p.units_per_seq;
-      r = reach(++c.b);
-    }
-    return r;
+  // To the unit that follows (the last one's successor is the last one).
+  auto move_on = [&](Place& x, Reach& r) {
+    if (++x.tile < p.row_tiles) return;
+    x.tile = 0;
+    if (++x.h < p.c.Hkv) return;
+    x.h = 0;
+    if (x.b < p.B - 1) r = reach(++x.b);
   };
   auto past_table = [&](const Reach& r) {
     if (r.n > 0 && r.start + r.n > r.keys && r.start + r.n > 0) atomicCAS(p.c.status, 0, FA_ERR_PAGE);
@@ -286,16 +276,16 @@ __global__ void __launch_bounds__(kThreads, (Shape<D, NT>::CtasPerSm)) fa_kv4_fw
   const long long worker = (long long)blockIdx.x * kWarps + warp;
   long long each = 0;
   int left = 0;   // steps (2^31 of them would be hours)
-  Cursor at{0, 0};
+  Place at{0, 0, 0};   // the unit at hand
+  int at_step = 0;     // and the step in it that comes next
   if constexpr (Near) {
-    const unsigned unit = blockIdx.x / (unsigned)p.cluster, u = unit % (unsigned)p.units_per_seq;
-    at.b = (int)(unit / (unsigned)p.units_per_seq);
+    const unsigned unit = blockIdx.x / (unsigned)p.cluster, tiles = (unsigned)p.row_tiles, heads = (unsigned)p.c.Hkv;
+    at = Place{(int)(unit / tiles / heads), (int)(unit / tiles % heads), (int)(unit % tiles)};
     const Reach r = reach(at.b);
-    if (u == 0 && threadIdx.x == 0) past_table(r);
+    if (at.h == 0 && at.tile == 0 && threadIdx.x == 0) past_table(r);
     const long long part = worker - (long long)unit * p.cluster * kWarps, parts = p.cluster * kWarps;
-    const int s0 = (int)(part * r.steps / parts);
-    left = (int)((part + 1) * r.steps / parts) - s0;
-    at.rem = (long long)u * r.steps + s0;
+    at_step = (int)(part * r.steps / parts);
+    left = (int)((part + 1) * r.steps / parts) - at_step;
   } else {
     const int per = (p.B + kThreads - 1) / kThreads;
     long long mine = 0;
@@ -342,29 +332,39 @@ __global__ void __launch_bounds__(kThreads, (Shape<D, NT>::CtasPerSm)) fa_kv4_fw
       return;
     }
     left = (int)(hi - lo);
-    at = Cursor{first * per, lo - first_sum};
-    settle(at);
+    long long rem = lo - first_sum;   // steps behind the first one of sequence at.b
+    at.b = first * per;
+    Reach r = reach(at.b);
+    while (rem >= r.steps * p.units_per_seq) {
+      rem -= r.steps * p.units_per_seq;
+      r = reach(++at.b);
+    }
+    const unsigned u = (unsigned)((unsigned long long)rem / (unsigned)r.steps);
+    at_step = (int)(rem - (long long)u * r.steps);
+    at.h = (int)(u / (unsigned)p.row_tiles);
+    at.tile = (int)(u % (unsigned)p.row_tiles);
   }
 
   // ---- the producer: lane i looks up block i % KB of step kBatch k + i / KB
   const int my_step = lane / KB;
   const uint32_t my_dst = ring0 + lane % KB * Block;
-  Cursor next{at.b, at.rem + my_step};
+  Place next = at;
+  Reach next_reach = reach(at.b);
+  int next_block = KB * at_step + lane;   // of the unit `next`, or as many behind it
   int page_next = -1, in_page_next = 0;
   const int per_page_shift = p.c.page_shift - 4;
   auto look_up = [&](bool there) {   // there: the step is this warp's
     page_next = -2;                  // no such block: nothing to copy
-    const Reach r = settle(next);
-    if (there) {
-      const unsigned u = unit_at(next.rem, r.steps);
-      const int blk = KB * (int)(next.rem - (long long)u * r.steps) + lane % KB;
-      if ((long long)blk * kKv4Block < r.keys) {
-        page_next = p.c.table[(size_t)next.b * p.c.max_pages + (size_t)(blk >> per_page_shift)];
-        if (page_next < 0) page_next = -1;
-        in_page_next = (int)((u / p.row_tiles) << per_page_shift) + (blk & ((1 << per_page_shift) - 1));
-      }
+    while (next_block >= KB * next_reach.steps) {
+      next_block -= KB * next_reach.steps;
+      move_on(next, next_reach);
     }
-    next.rem += kBatch;
+    if (there && (long long)next_block * kKv4Block < next_reach.keys) {
+      page_next = p.c.table[(size_t)next.b * p.c.max_pages + (size_t)(next_block >> per_page_shift)];
+      if (page_next < 0) page_next = -1;
+      in_page_next = (next.h << per_page_shift) + (next_block & ((1 << per_page_shift) - 1));
+    }
+    next_block += 32;
   };
   const uint8_t* src = nullptr;
   uint32_t bytes = 0;             // to copy: a block, or none
@@ -401,23 +401,21 @@ __global__ void __launch_bounds__(kThreads, (Shape<D, NT>::CtasPerSm)) fa_kv4_fw
   bool alive = true;
   int flying = 0;                              // stages on their way when a wait ran out
 
+  Reach r = reach(at.b);
   while (left > 0) {
     // ---- one unit's share
-    const Reach r = settle(at);
-    const unsigned u = unit_at(at.rem, r.steps);
-    const int s0 = (int)(at.rem - (long long)u * r.steps);
-    const int s1 = r.steps - s0 < left ? r.steps : s0 + left;
-    const int h = (int)(u / p.row_tiles), tile = (int)(u - (unsigned)h * p.row_tiles);
-    const long long row_in = (long long)tile * Sh::Rows;
-    const long long row0 = ((long long)at.b * p.H + (long long)h * group) * p.T + row_in;
+    const int s0 = at_step, s1 = r.steps - s0 < left ? r.steps : s0 + left;
+    const long long row_in = (long long)at.tile * Sh::Rows;
+    const long long row0 = ((long long)at.b * p.H + (long long)at.h * group) * p.T + row_in;
     const int rows = unit_rows - row_in < Sh::Rows ? (int)(unit_rows - row_in) : Sh::Rows;
     const bool begins = s0 == 0, ends = s1 == r.steps;
     const int left_then = left - (s1 - s0);
-    const long long unit = (long long)at.b * p.units_per_seq + u;
-    at.rem += s1 - s0;
+    const long long unit = ((long long)at.b * p.c.Hkv + at.h) * p.row_tiles + at.tile;
     if (!alive) {   // a wait ran out before: nothing to join
       if (!Near && begins && p.join_units && lane == 0) p.joins[unit].parts = 0;
       left = left_then;
+      at_step = 0;
+      move_on(at, r);
       continue;
     }
 
@@ -702,6 +700,8 @@ __global__ void __launch_bounds__(kThreads, (Shape<D, NT>::CtasPerSm)) fa_kv4_fw
     if (!alive) {
       if (!Near && begins && p.join_units && lane == 0) p.joins[unit].parts = 0;
       left = left_then;
+      at_step = 0;
+      move_on(at, r);
       continue;
     }
 
@@ -746,6 +746,8 @@ __global__ void __launch_bounds__(kThreads, (Shape<D, NT>::CtasPerSm)) fa_kv4_fw
         join = mine;
       }
     }
+    at_step = 0;
+    move_on(at, r);
   }
   if (!alive) {
     // copies in flight land before the CTA's shared memory goes
@@ -867,9 +869,10 @@ cudaError_t launch(Kv4FwdParams p, void* workspace, int sms, cudaStream_t st) {
 
   const int grid = (sms < kMaxSms ? sms : kMaxSms) * Sh::CtasPerSm;
   p.workers = grid * kWarps;
-  p.join_units = units <= p.workers;
-  // a row to a CTA of the joining kernel while that makes few CTAs
-  p.join_items = p.join_units && units * Sh::Rows <= 4096 ? D / 4 : kJoinThreads;
+  // many pieces a unit: a row to a CTA of the joining kernel, its threads on
+  // different pieces; else a CTA to each worker's last unit
+  p.join_units = units * 8 <= p.workers;
+  p.join_items = p.join_units ? D / 4 : kJoinThreads;
   p.joins = static_cast<Kv4Join*>(workspace);
   p.partials = reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + sizeof(Kv4Join) * kMaxSms * kWarps * 4);
   auto kern = fa_kv4_fwd_kernel<BF16, D, NT, false>;
