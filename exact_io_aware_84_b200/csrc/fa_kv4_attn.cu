@@ -21,12 +21,15 @@
 //     float32.  q goes in as fp16, its row's largest element brought to
 //     2^14 .. 2^15 by a power of two that the scale takes back: elements 2^-21
 //     of the row's largest or less round at 2^-36 of it.
+//     A row of up to four takes two columns, and one of two takes four (C).
 //   O^T = V^T P^T: the head's elements as rows.  V's codes become n by one
 //     fp16 subtraction, exactly: a sum over many keys must not carry an offset
 //     (taking it back by a product with -8 measured 6% slower).  P s_V is
 //     rounded to fp16, with s_V taken relative to the largest one so far (a
 //     power of two, which O's end takes back), and changes from accumulator to
-//     operand order by movmatrix.
+//     operand order by movmatrix.  A product's rows belong to one group of 32
+//     elements, as s_V does; with C > 1 they belong to two, and a row's columns
+//     hold P s_V for one group each, so that C times fewer are made.
 // The running maximum moves only when a score passes it by 2^8: P stays below
 // 2^8 and P s_V below 2^15.
 #include <cuda_runtime.h>
@@ -59,9 +62,9 @@ constexpr float kVPass = 128.f;              // with P below 2^8, P s_V stays in
 constexpr int kMostUp = 106;                 // P v_up stays finite
 constexpr float kLazy = 8.f;            // log2 by which a score may pass the running maximum
 
-template <int D, int NT>
+template <int D, int NT, int C>
 struct Shape {
-  static constexpr int W = D / 32, Rows = 8 * NT, Block = kv4_block_bytes(D);
+  static constexpr int W = D / 32, Rows = 8 * NT / C, Block = kv4_block_bytes(D);
   // Blocks of a step, CTAs a SM (as registers allow) and steps on their way to
   // a warp (as shared memory allows).
   static constexpr int Blocks = NT == 1 ? 4 : 2, Step = kKv4Block * Blocks;
@@ -79,6 +82,16 @@ __device__ __forceinline__ void mma16816(float (&d)[4], const uint32_t (&a)[4], 
       : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
       : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1), "f"(c[0]), "f"(c[1]), "f"(c[2]), "f"(c[3]));
 }
+
+__device__ __forceinline__ uint32_t hsub2(uint32_t a, uint32_t b) {
+  __half2 r = __hsub2(*reinterpret_cast<__half2*>(&a), *reinterpret_cast<__half2*>(&b));
+  return *reinterpret_cast<uint32_t*>(&r);
+}
+
+// The codes of places 0 and 2 (in units of 2^-24) and of places 1 and 3 (of
+// 2^-20) of a half-word, or of one shifted by 8, less their offset.
+__device__ __forceinline__ uint32_t code_even(uint32_t x) { return hsub2(x & 0x000f000fu, 0x00080008u); }
+__device__ __forceinline__ uint32_t code_odd(uint32_t x) { return hsub2(x & 0x00f000f0u, 0x00800080u); }
 
 // Of both half-words, the one of larger magnitude (its sign is of no use).
 template <bool BF16>
@@ -111,11 +124,6 @@ __device__ __forceinline__ uint32_t transpose8x8(uint32_t x) {
   uint32_t r;
   asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(x));
   return r;
-}
-
-__device__ __forceinline__ uint32_t hsub2(uint32_t a, uint32_t b) {
-  __half2 r = __hsub2(*reinterpret_cast<__half2*>(&a), *reinterpret_cast<__half2*>(&b));
-  return *reinterpret_cast<uint32_t*>(&r);
 }
 
 __device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_t bytes, uint32_t bar) {
@@ -188,9 +196,9 @@ __device__ __forceinline__ void cluster_sync() {
 
 // Joins the pieces that the warps of a cluster have left at the start of their
 // rings: the CTAs divide the unit's rows and columns.
-template <bool BF16, int D, int NT>
+template <bool BF16, int D, int NT, int C>
 __device__ __forceinline__ void join_in_cluster(const Kv4FwdParams& p, const uint8_t* ring_all) {
-  using Sh = Shape<D, NT>;
+  using Sh = Shape<D, NT, C>;
   __syncwarp();
   cluster_sync();
   const unsigned unit = blockIdx.x / (unsigned)p.cluster, rank = blockIdx.x % (unsigned)p.cluster;
@@ -227,9 +235,9 @@ __device__ __forceinline__ void join_in_cluster(const Kv4FwdParams& p, const uin
 
 // Near: a cluster of CTAs to a unit, whose warps divide its steps and whose
 // shared memory joins them.  Else all warps divide all steps.
-template <bool BF16, int D, int NT, bool Near>
-__global__ void __launch_bounds__(kThreads, (Shape<D, NT>::CtasPerSm)) fa_kv4_fwd_kernel(const Kv4FwdParams p) {
-  using Sh = Shape<D, NT>;
+template <bool BF16, int D, int NT, int C, bool Near>
+__global__ void __launch_bounds__(kThreads, (Shape<D, NT, C>::CtasPerSm)) fa_kv4_fwd_kernel(const Kv4FwdParams p) {
+  using Sh = Shape<D, NT, C>;
   constexpr int W = Sh::W, ST = Sh::Stages, KB = Sh::Blocks, Block = Sh::Block;
   constexpr int kBatch = 32 / KB;   // steps whose pages a warp looks up at once
   extern __shared__ __align__(128) uint8_t ring_all[];
@@ -240,6 +248,7 @@ __global__ void __launch_bounds__(kThreads, (Shape<D, NT>::CtasPerSm)) fa_kv4_fw
   long long* const chunk_sum = reinterpret_cast<long long*>(ring_all);   // until the first copies
 
   const int lane = threadIdx.x % 32, warp = threadIdx.x / 32, g = lane / 4, t = lane % 4;
+  const int column_class = t * C / 4;   // which of a row's C columns this lane's are
   uint8_t* const ring = ring_all + (size_t)warp * ST * Sh::Stage;
   float4* const less = reinterpret_cast<float4*>(ring_all + (size_t)kWarps * ST * Sh::Stage + warp * Sh::RowBytes) + t;
   const uint32_t bar0 = smem_u32(&bars[warp][0]), ring0 = smem_u32(ring);
@@ -433,8 +442,9 @@ __global__ void __launch_bounds__(kThreads, (Shape<D, NT>::CtasPerSm)) fa_kv4_fw
     };
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
-      const int my_lim = limit_of(8 * nt + g);
-      const uint4* qr = reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(p.q) + (row0 + 8 * nt + g) * D) + t;
+      const int my_row = 8 * nt + g % (8 / C);   // a row in each of its C columns
+      const int my_lim = limit_of(my_row);
+      const uint4* qr = reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(p.q) + (row0 + my_row) * D) + t;
       uint4 raw[W];
 #pragma unroll
       for (int e = 0; e < W; ++e) raw[e] = my_lim > 0 ? qr[4 * e] : make_uint4(0, 0, 0, 0);
@@ -653,40 +663,58 @@ __global__ void __launch_bounds__(kThreads, (Shape<D, NT>::CtasPerSm)) fa_kv4_fw
 #pragma unroll
         for (int bk = 0; bk < KB; ++bk) {
           const uint8_t* blk = base + bk * Block + 8 * D;
-          uint32_t vw[2][W], vs[2][W / 2];
+          uint32_t vw[2][W], b[NT][W / C][2];
+          float sv[2][W / C];   // the scales of this lane's groups
 #pragma unroll
           for (int half = 0; half < 2; ++half) {
+            const uint32_t* const scales = reinterpret_cast<const uint32_t*>(blk + 8 * D) + (half * 8 + g) * W + W / 2;
             if constexpr (W == 4) {
-              const uint2 y = reinterpret_cast<const uint2*>(blk + 8 * D)[2 * (half * 8 + g) + 1];
-              vs[half][0] = y.x, vs[half][1] = y.y;
               const uint4 x = reinterpret_cast<const uint4*>(blk)[half * 32 + lane];
               vw[half][0] = x.x, vw[half][1] = x.y, vw[half][2] = x.z, vw[half][3] = x.w;
             } else {
               const uint2 x = reinterpret_cast<const uint2*>(blk)[half * 32 + lane];
               vw[half][0] = x.x, vw[half][1] = x.y;
-              vs[half][0] = reinterpret_cast<const uint32_t*>(blk + 8 * D)[2 * (half * 8 + g) + 1];
+            }
+            if constexpr (W / C == 1) {
+              sv[half][0] = scale_half<BF16>(scales[column_class / 2] >> (16 * (column_class & 1)), 0);
+            } else if constexpr (W / C == 2) {
+              const uint32_t x = scales[C == 1 ? 0 : column_class];
+              sv[half][0] = scale_half<BF16>(x, 0), sv[half][1] = scale_half<BF16>(x, 1);
+            } else {
+              const uint2 x = *reinterpret_cast<const uint2*>(scales);
+              sv[half][0] = scale_half<BF16>(x.x, 0), sv[half][1] = scale_half<BF16>(x.x, 1);
+              sv[half][2] = scale_half<BF16>(x.y, 0), sv[half][3] = scale_half<BF16>(x.y, 1);
             }
           }
-          uint32_t b[NT][W][2];
 #pragma unroll
-          for (int e = 0; e < W; ++e) {
-            const float s0 = scale_half<BF16>(vs[0][e / 2], e & 1), s1 = scale_half<BF16>(vs[1][e / 2], e & 1);
+          for (int e = 0; e < W / C; ++e)
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt) {
               const float(&pr)[4] = sc[nt][bk];
-              b[nt][e][0] = transpose8x8(pack2<false>(pr[0] * s0, pr[1] * s0));
-              b[nt][e][1] = transpose8x8(pack2<false>(pr[2] * s1, pr[3] * s1));
+              b[nt][e][0] = transpose8x8(pack2<false>(pr[0] * sv[0][e], pr[1] * sv[0][e]));
+              b[nt][e][1] = transpose8x8(pack2<false>(pr[2] * sv[1][e], pr[3] * sv[1][e]));
             }
-          }
 #pragma unroll
           for (int e = 0; e < W; ++e) {
-            const uint32_t x0 = vw[0][e], x1 = vw[1][e], y0 = x0 >> 8, y1 = x1 >> 8;
-            const uint32_t a0[4] = {hsub2(x0 & 0x000f000fu, 0x00080008u), hsub2(x0 & 0x00f000f0u, 0x00800080u), hsub2(x1 & 0x000f000fu, 0x00080008u), hsub2(x1 & 0x00f000f0u, 0x00800080u)};
-            const uint32_t a1[4] = {hsub2(y0 & 0x000f000fu, 0x00080008u), hsub2(y0 & 0x00f000f0u, 0x00800080u), hsub2(y1 & 0x000f000fu, 0x00080008u), hsub2(y1 & 0x00f000f0u, 0x00800080u)};
+            uint32_t a0[4], a1[4];
+            if constexpr (C == 1) {
+              // group e: elements 4g and 4g + 1, 4g + 2 and 4g + 3
+              const uint32_t x0 = vw[0][e], x1 = vw[1][e], y0 = x0 >> 8, y1 = x1 >> 8;
+              a0[0] = code_even(x0), a0[1] = code_odd(x0), a0[2] = code_even(x1), a0[3] = code_odd(x1);
+              a1[0] = code_even(y0), a1[1] = code_odd(y0), a1[2] = code_even(y1), a1[3] = code_odd(y1);
+            } else {
+              // groups e / 2 and e / 2 + W / 2: element 4g + 2 (e % 2), and the one behind it
+              const int sh = 8 * (e % 2);
+              const uint32_t x0 = vw[0][e / 2] >> sh, x1 = vw[1][e / 2] >> sh;
+              const uint32_t y0 = vw[0][(e + W) / 2] >> sh, y1 = vw[1][(e + W) / 2] >> sh;
+              a0[0] = code_even(x0), a0[1] = code_even(y0), a0[2] = code_even(x1), a0[3] = code_even(y1);
+              a1[0] = code_odd(x0), a1[1] = code_odd(y0), a1[2] = code_odd(x1), a1[3] = code_odd(y1);
+            }
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt) {
-              mma16816(o[nt][e][0], a0, b[nt][e][0], b[nt][e][1], o[nt][e][0]);
-              mma16816(o[nt][e][1], a1, b[nt][e][0], b[nt][e][1], o[nt][e][1]);
+              const uint32_t(&bb)[2] = b[nt][C == 1 ? e : C == 2 ? e / 2 : 0];
+              mma16816(o[nt][e][0], a0, bb[0], bb[1], o[nt][e][0]);
+              mma16816(o[nt][e][1], a1, bb[0], bb[1], o[nt][e][1]);
             }
           }
         }
@@ -713,16 +741,28 @@ __global__ void __launch_bounds__(kThreads, (Shape<D, NT>::CtasPerSm)) fa_kv4_fw
     for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
       for (int c = 0; c < 2; ++c) {
-        const int row = 8 * nt + 2 * t + c;
+        const int row = 8 * nt + (2 * t + c) % (8 / C);
         float ll = quad_sum(l[nt][c]);
         if (row >= rows) continue;
         if (lim[nt][c] == 0) ll = 0.f;   // steps that all other rows see whole do not mask this one
         const float even = ll == 0.f ? 0.f : kUnit / ll, odd = even * 0.0625f;
 #pragma unroll
-        for (int e = 0; e < W; ++e) {
-          const float4 x = make_float4(o[nt][e][0][c] * even * v_down, o[nt][e][0][2 + c] * odd * v_down,
-                                       o[nt][e][1][c] * even * v_down, o[nt][e][1][2 + c] * odd * v_down);
-          const int col = 32 * e + 4 * g;
+        for (int e = 0; e < W; e += C == 1 ? 1 : 2) {
+          float4 x;
+          int group = e;
+          if constexpr (C == 1) {
+            x = make_float4(o[nt][e][0][c], o[nt][e][0][2 + c], o[nt][e][1][c], o[nt][e][1][2 + c]);
+          } else {
+            // of this tile's two groups the one that this lane's columns are for
+            const bool second = column_class >= C / 2;
+            group = e / 2 + (second ? W / 2 : 0);
+            if (C == 4 && group != column_class) continue;
+            x = second ? make_float4(o[nt][e][0][2 + c], o[nt][e][1][2 + c], o[nt][e + 1][0][2 + c], o[nt][e + 1][1][2 + c])
+                       : make_float4(o[nt][e][0][c], o[nt][e][1][c], o[nt][e + 1][0][c], o[nt][e + 1][1][c]);
+          }
+          x.x *= even, x.y *= odd, x.z *= even, x.w *= odd;
+          x.x *= v_down, x.y *= v_down, x.z *= v_down, x.w *= v_down;
+          const int col = 32 * group + 4 * g;
           if (part != nullptr)
             *reinterpret_cast<float4*>(part + row * D + col) = x;
           else if (p.o32)
@@ -731,7 +771,7 @@ __global__ void __launch_bounds__(kThreads, (Shape<D, NT>::CtasPerSm)) fa_kv4_fw
             *reinterpret_cast<uint2*>(static_cast<uint16_t*>(p.o) + (row0 + row) * D + col) =
                 make_uint2(pack2<BF16>(x.x, x.y), pack2<BF16>(x.z, x.w));
         }
-        if (g == 0) {
+        if (g == 0 && column_class == 0) {
           if (part != nullptr)
             *reinterpret_cast<float2*>(part + Sh::Rows * D + 2 * row) = make_float2(m[nt][c], ll);
           else
@@ -766,7 +806,7 @@ __global__ void __launch_bounds__(kThreads, (Shape<D, NT>::CtasPerSm)) fa_kv4_fw
       for (int i = lane; i < Sh::Rows; i += 32)
         *reinterpret_cast<float2*>(part + Sh::Rows * D + 2 * i) = make_float2(kLeast, 0.f);
     }
-    join_in_cluster<BF16, D, NT>(p, ring_all);
+    join_in_cluster<BF16, D, NT, C>(p, ring_all);
   }
 }
 
@@ -780,9 +820,9 @@ constexpr int kJoinThreads = 128;
 
 // It does not let the next kernel start early: an attention kernel's CTAs that
 // settle between this one's CTAs measured slower than ones that wait.
-template <bool BF16, int D, int NT>
+template <bool BF16, int D, int NT, int C>
 __global__ void __launch_bounds__(kJoinThreads) fa_kv4_join_kernel(const Kv4FwdParams p) {
-  using Sh = Shape<D, NT>;
+  using Sh = Shape<D, NT, C>;
   __shared__ Piece shared[kJoinThreads];
   grid_dependency_wait();
   const Kv4Join j = p.joins[blockIdx.x];
@@ -829,9 +869,6 @@ __global__ void __launch_bounds__(kJoinThreads) fa_kv4_join_kernel(const Kv4FwdP
 constexpr int kMaxSms = 160;
 constexpr int kNear = 8;
 
-// Query rows of a unit, in tiles of 8: what K's and V's decoding is shared by.
-int row_tiles_of(int d, long long rows) { return rows <= 8 ? 1 : rows <= 16 || d == 128 ? 2 : 4; }
-
 // Lets a kernel have its dynamic shared memory, once per device.
 template <typename Kernel>
 cudaError_t prepare(Kernel* kern, size_t smem, std::atomic<unsigned long long>* done) {
@@ -845,9 +882,9 @@ cudaError_t prepare(Kernel* kern, size_t smem, std::atomic<unsigned long long>* 
   return e;
 }
 
-template <bool BF16, int D, int NT>
+template <bool BF16, int D, int NT, int C>
 cudaError_t launch(Kv4FwdParams p, void* workspace, int sms, cudaStream_t st) {
-  using Sh = Shape<D, NT>;
+  using Sh = Shape<D, NT, C>;
   static std::atomic<unsigned long long> near_done{0}, far_done{0};
   cudaError_t e;
   const long long rows = (long long)(p.H / p.c.Hkv) * p.T;
@@ -862,7 +899,7 @@ cudaError_t launch(Kv4FwdParams p, void* workspace, int sms, cudaStream_t st) {
   while (cluster > 1 && (units * cluster > (long long)sms * Sh::CtasPerSm || cluster / 2 * kWarps >= most)) cluster /= 2;
   if (units * cluster <= (long long)sms * Sh::CtasPerSm && most <= (long long)cluster * kWarps * kNear) {
     p.cluster = cluster;
-    auto kern = fa_kv4_fwd_kernel<BF16, D, NT, true>;
+    auto kern = fa_kv4_fwd_kernel<BF16, D, NT, C, true>;
     if ((e = prepare(kern, Sh::Smem, &near_done)) != cudaSuccess) return e;
     return launch_chained_clusters(kern, dim3((unsigned)(units * cluster)), dim3(kThreads), Sh::Smem, st, cluster, p);
   }
@@ -875,32 +912,61 @@ cudaError_t launch(Kv4FwdParams p, void* workspace, int sms, cudaStream_t st) {
   p.join_items = p.join_units ? D / 4 : kJoinThreads;
   p.joins = static_cast<Kv4Join*>(workspace);
   p.partials = reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + sizeof(Kv4Join) * kMaxSms * kWarps * 4);
-  auto kern = fa_kv4_fwd_kernel<BF16, D, NT, false>;
+  auto kern = fa_kv4_fwd_kernel<BF16, D, NT, C, false>;
   if ((e = prepare(kern, Sh::Smem, &far_done)) != cudaSuccess) return e;
   if ((e = launch_chained(kern, dim3(grid), dim3(kThreads), Sh::Smem, st, p)) != cudaSuccess) return e;
   const dim3 join_grid(p.join_units ? (unsigned)units : (unsigned)p.workers,
                        (unsigned)((Sh::Rows * D / 4 + p.join_items - 1) / p.join_items));
-  return launch_chained(fa_kv4_join_kernel<BF16, D, NT>, join_grid, dim3(kJoinThreads), 0, st, p);
+  return launch_chained(fa_kv4_join_kernel<BF16, D, NT, C>, join_grid, dim3(kJoinThreads), 0, st, p);
 }
 
 }  // namespace
 
-size_t kv4_fwd_workspace(int d, long long rows) {
-  const int nt = row_tiles_of(d, rows);
-#define FA_KV4(DD, NN) (size_t)Shape<DD, NN>::CtasPerSm * kWarps * 2 * Shape<DD, NN>::Slot * 4
-  const size_t a_sm = d == 128 ? (nt == 1 ? FA_KV4(128, 1) : FA_KV4(128, 2))
-                               : (nt == 1 ? FA_KV4(64, 1) : nt == 2 ? FA_KV4(64, 2) : FA_KV4(64, 4));
-#undef FA_KV4
-  return sizeof(Kv4Join) * kMaxSms * kWarps * 4 + kMaxSms * a_sm;
+// Query rows that share a key head go in tiles of 8 columns: one row in two or
+// four columns where rows are few, up to four tiles a unit where they are many.
+template <typename F>
+static auto kv4_variant(int d, long long rows, F&& f) {
+  if (d == 128) {
+    if (rows <= 2) return f.template operator()<128, 1, 4>();
+    if (rows <= 4) return f.template operator()<128, 1, 2>();
+    if (rows <= 8) return f.template operator()<128, 1, 1>();
+    return f.template operator()<128, 2, 1>();
+  }
+  if (rows <= 4) return f.template operator()<64, 1, 2>();
+  if (rows <= 8) return f.template operator()<64, 1, 1>();
+  if (rows <= 16) return f.template operator()<64, 2, 1>();
+  return f.template operator()<64, 4, 1>();
 }
 
+namespace {
+
+struct Workspace {
+  template <int D, int NT, int C>
+  size_t operator()() const {
+    return sizeof(Kv4Join) * kMaxSms * kWarps * 4 +
+           (size_t)kMaxSms * Shape<D, NT, C>::CtasPerSm * kWarps * 2 * Shape<D, NT, C>::Slot * 4;
+  }
+};
+
+struct Launch {
+  bool bf16;
+  const Kv4FwdParams& p;
+  void* workspace;
+  int sms;
+  cudaStream_t st;
+
+  template <int D, int NT, int C>
+  cudaError_t operator()() const {
+    return bf16 ? launch<true, D, NT, C>(p, workspace, sms, st) : launch<false, D, NT, C>(p, workspace, sms, st);
+  }
+};
+
+}  // namespace
+
+size_t kv4_fwd_workspace(int d, long long rows) { return kv4_variant(d, rows, Workspace{}); }
+
 cudaError_t launch_kv4_fwd(bool bf16, int d, const Kv4FwdParams& p, void* workspace, int sms, cudaStream_t st) {
-  const int nt = row_tiles_of(d, (long long)(p.H / p.c.Hkv) * p.T);
-#define FA_KV4(DD, NN) \
-  (bf16 ? launch<true, DD, NN>(p, workspace, sms, st) : launch<false, DD, NN>(p, workspace, sms, st))
-  if (d == 128) return nt == 1 ? FA_KV4(128, 1) : FA_KV4(128, 2);
-  return nt == 1 ? FA_KV4(64, 1) : nt == 2 ? FA_KV4(64, 2) : FA_KV4(64, 4);
-#undef FA_KV4
+  return kv4_variant(d, (long long)(p.H / p.c.Hkv) * p.T, Launch{bf16, p, workspace, sms, st});
 }
 
 }  // namespace fa

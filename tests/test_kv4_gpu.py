@@ -413,7 +413,7 @@ def _room(c, positions=1 << 17):
 
 @pytest.mark.parametrize("dtype", ["bf16", "fp16"])
 @pytest.mark.parametrize("d", [64, 128])
-@pytest.mark.parametrize("H,Hkv", [(2, 2), (8, 1), (12, 4), (5, 1), (33, 1)])
+@pytest.mark.parametrize("H,Hkv", [(2, 2), (8, 1), (12, 4), (4, 2), (5, 1), (33, 1)])
 @pytest.mark.parametrize("T,causal", [(1, True), (3, True), (3, False)])
 def test_room_for_long_sequences(T, causal, H, Hkv, d, dtype):
     start = [0, 14, 900]
