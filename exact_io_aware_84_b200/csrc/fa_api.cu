@@ -598,6 +598,7 @@ int fa_fwd_kv4(const void* q, const void* pool, const int* page_table, const int
   p.causal = causal != 0;
   p.o32 = dtype == FA_BF16_O_F32 || dtype == FA_FP16_O_F32;
   p.wait_limit_ns = wait_limit_ns();
+  p.debug_flags = g_debug_flags.load();
   const cudaError_t e = launch_kv4_fwd(dtype == FA_BF16 || dtype == FA_BF16_O_F32, d, p, workspace, di.sms,
                                        static_cast<cudaStream_t>(stream));
   return e == cudaSuccess ? FA_OK : FA_ERR_CUDA;

@@ -177,6 +177,7 @@ struct Kv4FwdParams {
   int causal;
   int o32;
   uint64_t wait_limit_ns;
+  int debug_flags;     // bit 2: withhold one arrival (timeout test)
   // set by the launch
   int row_tiles;             // tiles of query rows a key head
   long long units_per_seq;   // Hkv * row_tiles

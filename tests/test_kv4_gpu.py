@@ -590,3 +590,52 @@ def test_a_binding_made_workspace_and_outputs_on_a_side_stream():
     assert torch.equal(want[0], got[0]) and torch.equal(want[1], got[1])
     assert np.array_equal(to64(k)[0, 0, 0], round16_ref(c.k[0, 0, 899], "fp16"))
     _ok()
+
+
+def test_what_a_call_allocates_belongs_to_its_stream():
+    """A block that the current stream has freed but not finished reading is not
+    what a call on another stream writes to."""
+    c = Cache(1, 2, 128, "bf16", 16, 4096, seed=30)
+    c.write([0], 4096)
+    start, q = _ints([4095]), _rows(c.g, "bf16", 1, 8, 1, 128).cuda()
+    want = fa.fa_fwd_kv4(q, c.pool, c.table, start)
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    need = fa.fa_fwd_kv4_workspace_size(1, 8, 2, 1, 128)
+    for go in (lambda s: fa.fa_kv4_read(c.pool, c.table, _ints([0]), N=4096, dtype=torch.bfloat16, stream=s),
+               lambda s: fa.fa_fwd_kv4(q, c.pool, c.table, start, stream=s)):
+        for stream in (side, side.cuda_stream):
+            torch.cuda.empty_cache()
+            a = torch.full((2 * 4096 * 128,), 3.0, dtype=torch.bfloat16, device="cuda")
+            b = torch.full((need,), 5, dtype=torch.uint8, device="cuda")
+            torch.cuda.synchronize()
+            torch.cuda._sleep(20_000_000)            # the current stream is busy, then reads a and b
+            a2, b2 = a + 0, b + 0
+            del a, b
+            got = go(stream)
+            torch.cuda.synchronize()
+            assert (a2 == 3).all() and (b2 == 5).all()
+            if got[0].shape == want[0].shape:
+                assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+    _ok()
+
+
+@pytest.mark.parametrize("wide", [False, True])
+def test_a_withheld_arrival_ends_with_a_status(wide):
+    c = Cache(2, 2, 128, "bf16", 16, 2100, seed=31)
+    c.write([0, 0], 2100)
+    if wide:
+        _room(c)
+    q = _rows(c.g, "bf16", 2, 8, 1, 128)
+    _ok()
+    assert fa.fa_debug_set_wait_limit_ms(100) == fa.FA_OK
+    assert fa.fa_debug_set_flags(4) == fa.FA_OK
+    try:
+        fa.fa_fwd_kv4(q.cuda(), c.pool, c.table, _ints([2099, 900]))
+        assert fa.fa_last_device_status() == fa.FA_ERR_TIMEOUT
+        assert fa.fa_last_device_status() == fa.FA_OK
+    finally:
+        fa.fa_debug_set_flags(0)
+        fa.fa_debug_set_wait_limit_ms(1000)
+    c.check_attention(q, [2099, 900])
+    _ok()
