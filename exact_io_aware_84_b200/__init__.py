@@ -11,7 +11,6 @@ sm_100 device is present, the calls raise.
 
 from __future__ import annotations
 
-import contextlib
 import ctypes
 import os
 from typing import Optional
@@ -538,7 +537,7 @@ def _check_kv4(pool, page_table, start, count, like, B, Hkv, d):
     table_shape = page_table.shape
     if len(table_shape) != 2 or table_shape[0] != B:
         raise ValueError(f"page_table must be [B, max_pages] with B = {B}")
-    int32, per_sequence = torch.int32, (B,)
+    int32 = torch.int32
     for name, t in (("page_table", page_table), ("start", start), ("count", count)):
         if t is None and name == "count":
             continue
@@ -546,26 +545,24 @@ def _check_kv4(pool, page_table, start, count, like, B, Hkv, d):
             raise ValueError(f"{name} must be a contiguous CUDA int32 tensor")
         if t.device != device:
             raise ValueError(f"{name} is on {t.device}, the rows on {device}: they must share a device")
-        if t is not page_table and t.shape != per_sequence:
+        if t is not page_table and (t.dim() != 1 or t.shape[0] != B):
             raise ValueError(f"{name} must be [B] with B = {B}")
     if pool.device != device:
         raise ValueError(f"pool is on {pool.device}, the rows on {device}: they must share a device")
     return n_pages, 16 * blocks, table_shape[1]
 
 
-_NO_CONTEXT = contextlib.nullcontext()
-
-
-def _allocating_on(stream, device):
-    """Context in which what a call allocates belongs to the stream that it runs
-    on: memory of another stream could still be in use there, or be given away
-    before the call's kernels are done with it."""
+def _allocating_on(stream, device, allocate):
+    """allocate(), with what it allocates belonging to the stream that the call
+    runs on: memory of another stream could still be in use there, or be given
+    away before the call's kernels are done with it."""
     if stream is None:
-        return _NO_CONTEXT
+        return allocate()
     torch = _torch()
     if not isinstance(stream, torch.cuda.Stream):
         stream = torch.cuda.ExternalStream(_stream_handle(stream, device), device=device)
-    return torch.cuda.stream(stream)
+    with torch.cuda.stream(stream):
+        return allocate()
 
 
 def _kv4_call(where, device, stream, fn, *args):
@@ -614,9 +611,7 @@ def fa_kv4_read(pool, page_table, start, count=None, N: Optional[int] = None, k=
         if N is None or dtype not in (torch.bfloat16, torch.float16):
             raise ValueError("without k and v, give N and dtype (bfloat16 or float16)")
         shape = (page_table.shape[0], pool.shape[1], N, pool.shape[3] // 18)
-        with _allocating_on(stream, pool.device):
-            k = pool.new_empty(shape, dtype=dtype)
-            v = torch.empty_like(k)
+        k, v = _allocating_on(stream, pool.device, lambda: [pool.new_empty(shape, dtype=dtype) for _ in range(2)])
     else:
         _check_bhnd("k", k)
         _check_bhnd("v", v)
@@ -663,14 +658,13 @@ def fa_fwd_kv4(q, pool, page_table, start, count=None, o=None, lse=None, workspa
         _check_workspace(workspace, q)
     lib = load_library()
     if o is None or lse is None or workspace is None:
-        with _allocating_on(stream, q.device):
-            if o is None:
-                o = torch.empty_like(q, dtype=torch.float32) if o_fp32 else torch.empty_like(q)
-            if lse is None:
-                lse = q.new_empty((B, H, T), dtype=torch.float32)
-            if workspace is None:
-                need = int(lib.fa_fwd_kv4_workspace_size(B, H, Hkv, T, d))
-                workspace = torch.empty(need, dtype=torch.uint8, device=q.device)
+        def allocate():
+            need = 0 if workspace is not None else int(lib.fa_fwd_kv4_workspace_size(B, H, Hkv, T, d))
+            return (o if o is not None else torch.empty_like(q, dtype=torch.float32) if o_fp32 else torch.empty_like(q),
+                    lse if lse is not None else q.new_empty((B, H, T), dtype=torch.float32),
+                    workspace if workspace is not None else q.new_empty((need,), dtype=torch.uint8))
+
+        o, lse, workspace = _allocating_on(stream, q.device, allocate)
     _kv4_call("fa_fwd_kv4", q.device, stream, lib.fa_fwd_kv4, q.data_ptr(), pool.data_ptr(), page_table.data_ptr(),
               start.data_ptr(), None if count is None else count.data_ptr(), o.data_ptr(), lse.data_ptr(),
               workspace.data_ptr(), workspace.numel() * workspace.element_size(), B, H, Hkv, T, d, n_pages, page,
