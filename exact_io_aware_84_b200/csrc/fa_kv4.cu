@@ -195,25 +195,24 @@ __global__ void __launch_bounds__(kThreads) fa_kv4_write_kernel(const WriteParam
   if (blk == nullptr) return;
   auto there = [&](int key) { return first + key >= 0 && first + key < r.n; };
 
-  uint4 x[2][2 * W];   // by half: K's groups, then V's
-#pragma unroll
-  for (int half = 0; half < 2; ++half)
-#pragma unroll
-    for (int j = 0; j < 2 * W; ++j) {
-      x[half][j] = make_uint4(0, 0, 0, 0);
-      if (there(half * 8 + g)) {
-        const uint4* rows = j < W ? p.k : p.v;
-        x[half][j] = rows[((size_t)r.bh * p.T + (size_t)(first + half * 8 + g)) * (D / 8) + 4 * (j % W) + t];
-      }
-    }
-#pragma unroll
+  // One half at a time: with both in flight fewer warps are, and 2 x 16 heads x
+  // 8192 x 128 took 33 us instead of 28.
+#pragma unroll 1
   for (int half = 0; half < 2; ++half) {
     if (first + half * 8 >= r.n || first + half * 8 + 8 <= 0) continue;
     const bool mine = there(half * 8 + g);
+    uint4 x[2 * W];
+#pragma unroll
+    for (int j = 0; j < 2 * W; ++j) {
+      x[j] = make_uint4(0, 0, 0, 0);
+      const size_t row = (size_t)r.bh * p.T + (size_t)(first + half * 8 + g);
+      if (mine) x[j] = (j < W ? p.k : p.v)[row * (D / 8) + 4 * (j % W) + t];
+    }
+
     uint32_t word[2 * W];
 #pragma unroll
     for (int q = 0; q < W / 2; ++q) {   // four groups at a time
-      uint4 (&x4)[4] = *reinterpret_cast<uint4(*)[4]>(&x[half][4 * q]);
+      uint4 (&x4)[4] = *reinterpret_cast<uint4(*)[4]>(&x[4 * q]);
       uint32_t (&w4)[4] = *reinterpret_cast<uint32_t(*)[4]>(&word[4 * q]);
       const uint16_t s = quantise4<BF16>(x4, w4, lane);
       if (mine) reinterpret_cast<uint16_t*>(blk + 16 * D)[(half * 8 + g) * 2 * W + 4 * q + t] = s;
