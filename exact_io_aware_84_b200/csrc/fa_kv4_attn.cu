@@ -4,24 +4,29 @@
 // P = softmax over the keys j that the row may see, O = sum_j P_j s_V n_V.
 // The codes are used as they stand, never rounded to 16 bits.
 //
-// Work.  A unit is one key head's tile of NT * 8 query rows; its keys are cut
-// into steps of 32.  The steps of all units, laid end to end, are divided
-// evenly over the grid's warps (lengths are known on the device only, so each
-// CTA sums them up first).  A warp that holds a unit from its first to its
-// last step writes the result; the pieces of a unit that lies across warps go
-// to the workspace, and a second kernel joins them.  Sums are in a fixed
-// order: the same call gives the same bits.
+// Work.  A unit is one key head's tile of up to NT * 8 query rows; its keys
+// are cut into steps of 64 (NT = 1) or 32.  Lengths are known on the device
+// only.  Two divisions:
+//   near: a cluster of up to 8 CTAs to a unit, whose warps take equal shares
+//     of its steps and which joins them through distributed shared memory.
+//     For few and short units: one kernel, no plan, no trip through memory.
+//   far: the steps of all units, laid end to end, are divided evenly over the
+//     warps of a grid that fills the GPU once (each CTA sums the lengths up
+//     first).  A warp that holds a unit from its first to its last step writes
+//     the result; the pieces of a unit that lies across warps go to the
+//     workspace, and a second kernel joins them.
+// Sums are in a fixed order: the same call gives the same bits.
 //
-// A step.  The two blocks of 16 keys come by asynchronous bulk copy into a
-// ring that belongs to the warp, ST steps deep, so no warp waits for another.
+// A step.  Its blocks of 16 keys come by asynchronous bulk copy into a ring
+// that belongs to the warp, so no warp waits for another.
 //   S^T = K Q^T by mma.m16n8k16, keys as rows and 8 query rows as columns:
 //     nothing is wasted when four or eight query heads share a key head.  A
 //     code c = n + 8 enters as the fp16 subnormal that its nibble is; each
 //     group's sum of 32 starts at -8 times the sum of q and is then scaled in
 //     float32.  q goes in as fp16, its row's largest element brought to
-//     2^14 .. 2^15 by a power of two that the scale takes back: elements 2^-21
-//     of the row's largest or less round at 2^-36 of it.
-//     A row of up to four takes two columns, and one of two takes four (C).
+//     2^14 .. 2^15 by a power of two that the scale takes back: elements below
+//     2^-24 of the row's largest round, at 2^-35 of it.  Where four or two rows
+//     are all there are, each takes C = 2 or 4 columns.
 //   O^T = V^T P^T: the head's elements as rows.  V's codes become n by one
 //     fp16 subtraction, exactly: a sum over many keys must not carry an offset
 //     (taking it back by a product with -8 measured 6% slower).  P s_V is
@@ -32,6 +37,17 @@
 //     hold P s_V for one group each, so that C times fewer are made.
 // The running maximum moves only when a score passes it by 2^8: P stays below
 // 2^8 and P s_V below 2^15.
+//
+// What bounds it.  Reading the cache once: 9D/8 bytes a key and key head.  At
+// d = 128 and up to 8 rows a warp issues about 240 instructions and 16 products
+// for 16 keys; with 12 warps a SM that is about 90 SM cycles where memory
+// needs 100, and the two overlap.  Measured on B200 (graph of calls): 8
+// sequences of 65536 keys and 8 rows 115 us, 5.3 TB/s; 64 sequences of up to
+// 8192 keys and 4 rows 73 us, 4.5 TB/s, about 15 us of both being the
+// start, the ends of units and the joining kernel; one sequence of 1000 keys
+// 8.0 us.  A product costs its pipe 8.5 cycles a SM quarter and delays the
+// integer instructions beside it (4 of them and 4 half-precision ones: 12.8),
+// so 24 products in place of 32 subtractions lost.
 #include <cuda_runtime.h>
 
 #include <atomic>
@@ -812,11 +828,12 @@ __global__ void __launch_bounds__(kThreads, (Shape<D, NT, C>::CtasPerSm)) fa_kv4
 
 // O and LSE of the units that lie across workers.  Pieces are normalised, with
 // their maximum m (in log2) and sum l beside them; a piece that saw no key has
-// l = 0.  A CTA joins a row, or 128 fours of elements, of a unit; records are
-// kept by unit, or, where units are more than workers, for the unit that
-// begins in a worker and goes on behind it.  Threads to spare take the pieces
-// in turn, eight at a time in flight.
-constexpr int kJoinThreads = 128;
+// l = 0.  Where a unit has many pieces, records are kept by unit and a CTA of
+// 256 threads joins a row of one; else they are kept for the unit that begins
+// in a worker and goes on behind it, and one of 128 threads joins 128 fours of
+// its elements.  Threads to spare take the pieces in turn, eight at a time in
+// flight.
+constexpr int kJoinThreads = 256;   // at most
 
 // It does not let the next kernel start early: an attention kernel's CTAs that
 // settle between this one's CTAs measured slower than ones that wait.
@@ -829,7 +846,7 @@ __global__ void __launch_bounds__(kJoinThreads) fa_kv4_join_kernel(const Kv4FwdP
   const int first = blockIdx.y * p.join_items;
   if (j.parts == 0 || j.rows * (D / 4) <= first) return;
   const int worker = j.worker;
-  const int items = min(j.rows * (D / 4) - first, p.join_items), turns = min(kJoinThreads / items, j.parts + 1);
+  const int items = min(j.rows * (D / 4) - first, p.join_items), turns = min((int)blockDim.x / items, j.parts + 1);
   const int item = threadIdx.x % items, turn = threadIdx.x / items;
   const int row = (first + item) / (D / 4), col = 4 * ((first + item) % (D / 4));
   Piece sum{make_float4(0.f, 0.f, 0.f, 0.f), kLeast, 0.f};
@@ -867,6 +884,10 @@ __global__ void __launch_bounds__(kJoinThreads) fa_kv4_join_kernel(const Kv4FwdP
 }
 
 constexpr int kMaxSms = 160;
+// Most steps a warp for which a cluster a unit is the better division: 8 key
+// heads of one sequence, d = 128, four query heads each, take 13.4 us over 8192
+// keys (4 steps) and 18.5 over 16384 (8), the other division 19.6 and 22.4; of
+// four sequences over 16384 keys it takes 27.8 where clusters take 29.6.
 constexpr int kNear = 8;
 
 // Lets a kernel have its dynamic shared memory, once per device.
@@ -906,10 +927,12 @@ cudaError_t launch(Kv4FwdParams p, void* workspace, int sms, cudaStream_t st) {
 
   const int grid = (sms < kMaxSms ? sms : kMaxSms) * Sh::CtasPerSm;
   p.workers = grid * kWarps;
-  // many pieces a unit: a row to a CTA of the joining kernel, its threads on
-  // different pieces; else a CTA to each worker's last unit
-  p.join_units = units * 8 <= p.workers;
-  p.join_items = p.join_units ? D / 4 : kJoinThreads;
+  // Few rows in all, and so many pieces to each: a row to a CTA of the joining
+  // kernel.  Else a CTA to each worker's last unit.  (64 units of 8 rows, 28
+  // pieces each: 115 us by row, 117 by worker; 96 units of 16 rows, 19 pieces:
+  // 44.5 and 40.5.)
+  p.join_units = units * Sh::Rows <= 4ll * sms;
+  p.join_items = p.join_units ? D / 4 : 128;
   p.joins = static_cast<Kv4Join*>(workspace);
   p.partials = reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + sizeof(Kv4Join) * kMaxSms * kWarps * 4);
   auto kern = fa_kv4_fwd_kernel<BF16, D, NT, C, false>;
@@ -917,13 +940,18 @@ cudaError_t launch(Kv4FwdParams p, void* workspace, int sms, cudaStream_t st) {
   if ((e = launch_chained(kern, dim3(grid), dim3(kThreads), Sh::Smem, st, p)) != cudaSuccess) return e;
   const dim3 join_grid(p.join_units ? (unsigned)units : (unsigned)p.workers,
                        (unsigned)((Sh::Rows * D / 4 + p.join_items - 1) / p.join_items));
-  return launch_chained(fa_kv4_join_kernel<BF16, D, NT, C>, join_grid, dim3(kJoinThreads), 0, st, p);
+  return launch_chained(fa_kv4_join_kernel<BF16, D, NT, C>, join_grid, dim3(p.join_units ? kJoinThreads : 128),
+                        0, st, p);
 }
 
 }  // namespace
 
-// Query rows that share a key head go in tiles of 8 columns: one row in two or
-// four columns where rows are few, up to four tiles a unit where they are many.
+// Query rows that share a key head go in tiles of 8 columns.  One row in two
+// columns where four rows share a head: 64 sequences of up to 8192 keys, d =
+// 128, 73.7 us against 77.7.  Two tiles a unit where more than 8 rows do: 64
+// sequences of 4096 keys and 12 rows, 106 us against 119 with one.  (Four,
+// where registers allow them at d = 64, lost: 18.4 against 14.8 us for two
+// sequences of 3000 keys and 384 rows a head.)
 template <typename F>
 static auto kv4_variant(int d, long long rows, F&& f) {
   if (d == 128) {
@@ -934,8 +962,7 @@ static auto kv4_variant(int d, long long rows, F&& f) {
   }
   if (rows <= 4) return f.template operator()<64, 1, 2>();
   if (rows <= 8) return f.template operator()<64, 1, 1>();
-  if (rows <= 16) return f.template operator()<64, 2, 1>();
-  return f.template operator()<64, 4, 1>();
+  return f.template operator()<64, 2, 1>();
 }
 
 namespace {
