@@ -318,9 +318,13 @@ int fa_fwd_fp8(const void* q, const void* k, const void* v, void* o, float* lse,
  *   sequence that have been written already.  Query t sees the keys
  *   0 .. start[b] + t when `causal` is set, else 0 .. start[b] + count[b] - 1.
  *   Padding rows and rows that see no key get O = 0, LSE = -inf.  n s enters
- *   unrounded; P s is rounded to fp16 before the product with V's codes, sums
- *   are float32.  o, lse, scale as in fa_fwd ([B,H,T,d], [B,H,T]; the *_O_F32
- *   codes store O in float32, as fa_merge takes it).
+ *   unrounded and sums are float32; q is taken relative to its row's largest
+ *   element and rounded at 2^-35 of it (elements above 2^-24 of it are exact),
+ *   and P s is rounded to fp16, relative to V's largest scale, before the
+ *   product with V's codes.  o, lse, scale as in fa_fwd ([B,H,T,d], [B,H,T];
+ *   the *_O_F32 codes store O in float32, as fa_merge takes it).  Any T: what
+ *   the cache holds is read once per 8 or 16 rows of the T * H / Hkv that share
+ *   a key head, so fa_kv4_read and fa_fwd_gqa suit whole prompts better.
  *   workspace: device buffer of fa_fwd_kv4_workspace_size bytes, 256-byte
  *   aligned, contents ignored on entry; calls that may overlap on the GPU need
  *   one each.
