@@ -646,9 +646,9 @@ __global__ void __launch_bounds__(kThreads, (Shape<D, NT, C>::CtasPerSm)) fa_kv4
           for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
             for (int c = 0; c < 2; ++c) {
-              const float mx = f[nt][c] * quad_max(top[nt][c]);
+              const float best = quad_max(top[nt][c]), mx = f[nt][c] * best;
               float fm = 1.f;
-              if (mx - m[nt][c] > kLazy) {
+              if (fmaf(best, f[nt][c], -m[nt][c]) > kLazy) {   // as above: no other row has a say in it
                 fm = ex2_approx(m[nt][c] - mx);
                 m[nt][c] = mx;
                 l[nt][c] *= fm;

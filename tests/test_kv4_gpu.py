@@ -180,6 +180,38 @@ def test_values_that_quantisers_trip_over(dtype):
     _ok()
 
 
+@pytest.mark.parametrize("dtype", ["bf16", "fp16"])
+def test_every_ratio_of_mantissas_rounds_as_defined(dtype):
+    """Every mantissa of the largest element against every other mantissa, at the exponents where codes differ, both
+    signs: a group holds its largest element and 31 others."""
+    t = TYPES[dtype]
+    m = 128 if dtype == "bf16" else 1024
+    mant = 1 + torch.arange(m, dtype=torch.float64, device="cuda") / m
+    others = (mant[None, :] * 2.0 ** -torch.arange(6, dtype=torch.float64, device="cuda")[:, None]).flatten()
+    others = torch.cat([others, -others])
+    others = torch.cat([others, others.new_zeros(-len(others) % 31)]).reshape(-1, 31)          # [g, 31]
+    for sign in (1.0, -1.0):
+        x = torch.empty(m, len(others), 32, dtype=torch.float64, device="cuda")
+        x[:, :, 0] = sign * mant[:, None]
+        x[:, :, 1:] = torch.where(others.abs()[None] <= mant[:, None, None], others[None], 0.0)
+        rows = x.reshape(-1)
+        rows = torch.cat([rows, rows.new_zeros(-len(rows) % 128)]).reshape(1, 1, -1, 128).to(t)  # exact
+        n = rows.shape[2]
+        page = 256
+        pool = fa.fa_kv4_pool(-(-n // page), 1, page, 128)
+        table = torch.arange(pool.shape[0], dtype=torch.int32, device="cuda").flip(0).reshape(1, -1).contiguous()
+        fa.fa_kv4_write(rows, rows.flip(2).contiguous(), pool, table, _ints([0]))
+        k, v = fa.fa_kv4_read(pool, table, _ints([0]), N=n, dtype=t)
+        g = rows.double().reshape(-1, 32)
+        hi, lo = g.amax(1), g.amin(1)
+        s = (torch.where(hi > -lo, hi, lo) / -8).to(t).double()[:, None]
+        code = torch.where(s == 0, 0.0, torch.floor((2 * g / torch.where(s == 0, 1.0, s) + 1) / 2).clamp(-8, 7))
+        # 2 g / s + 1 in float64 is within 2^-49 of a ratio that is a whole number or 2^-12 away from one
+        want = (code * s).to(t).reshape(rows.shape)
+        assert torch.equal(k, want) and torch.equal(v, want.flip(2))
+    _ok()
+
+
 def test_reading_leaves_the_cache_and_its_neighbours_alone():
     c = Cache(2, 2, 128, "bf16", 16, 50, seed=8)
     c.write([0, 0], 50)
@@ -448,13 +480,13 @@ def test_room_and_several_new_tokens(T, d):
 @pytest.mark.parametrize("wide", [False, True])
 def test_more_units_than_warps(wide):
     """2400 key heads of short sequences, some of them empty."""
-    B = 1200
-    c = Cache(B, 2, 64, "bf16", 64, 64, seed=27)
+    B = 300
+    c = Cache(B, 8, 64, "bf16", 64, 64, seed=27)
     c.write([0] * B, 64)
     if wide:
         _room(c, 1 << 12)
     count = [0 if b % 11 == 3 else 1 for b in range(B)]
-    c.check_attention(_rows(c.g, "bf16", B, 2, 1, 64), [(b * 7) % 64 for b in range(B)], count=count)
+    c.check_attention(_rows(c.g, "bf16", B, 8, 1, 64), [(b * 7) % 64 for b in range(B)], count=count)
     _ok()
 
 
