@@ -552,6 +552,28 @@ def _check_kv4(pool, page_table, start, count, like, B, Hkv, d):
     return n_pages, 16 * blocks, table_shape[1]
 
 
+_SERVE = None
+
+
+def _compiled(t):
+    """The compiled binding of the serving calls, or None for what is not a
+    CUDA tensor or where it has not been built.  Its functions return None for
+    arguments that they do not take."""
+    global _SERVE
+    if _SERVE is None:
+        if type(t) is not _torch().Tensor or not t.is_cuda:
+            return None
+        path = os.path.join(os.path.dirname(os.path.abspath(__file__)), "_serve.so")
+        if not os.path.exists(path):
+            return None
+        lib = load_library()
+        from . import _serve as module
+        module.connect(*(ctypes.cast(getattr(lib, name), _vp).value
+                         for name in ("fa_kv4_write", "fa_kv4_read", "fa_fwd_kv4", "fa_fwd_kv4_workspace_size")))
+        _SERVE = module
+    return _SERVE
+
+
 def _allocating_on(stream, device, allocate):
     """allocate(), with what it allocates belonging to the stream that the call
     runs on: memory of another stream could still be in use there, or be given
@@ -585,6 +607,12 @@ def fa_kv4_write(k, v, pool, page_table, start, count=None, stream=None):
 
     page_table: int32 [B, max_pages]; start, count: int32 [B].
     """
+    if stream is None and (serve := _compiled(k)) is not None:
+        st = serve.write(k, v, pool, page_table, start, count)
+        if st is not None:
+            if st != FA_OK:
+                raise FAError(st, "fa_kv4_write")
+            return
     _check_bhnd("k", k)
     _check_bhnd("v", v)
     if v.shape != k.shape or v.dtype != k.dtype or v.device != k.device:
@@ -602,6 +630,12 @@ def fa_kv4_read(pool, page_table, start, count=None, N: Optional[int] = None, k=
     4-bit cache, rows at and after count[b] zero.  ``k`` and ``v`` may be
     preallocated, else N and ``dtype`` (the type that was written) say what
     to allocate."""
+    if stream is None and k is None and v is None and (serve := _compiled(pool)) is not None:
+        out = serve.read(pool, page_table, start, count, N, dtype)
+        if out is not None:
+            if isinstance(out, int):
+                raise FAError(out, "fa_kv4_read")
+            return out
     torch = _torch()
     if pool.dim() != 4:
         raise ValueError("pool must be [n_pages, Hkv, page/16, 18 d]")
@@ -641,6 +675,12 @@ def fa_fwd_kv4(q, pool, page_table, start, count=None, o=None, lse=None, workspa
     A decoding step: fa_kv4_write(k, v, pool, table, start), then
     fa_fwd_kv4(q, pool, table, start), then start += 1.
     """
+    if stream is None and (serve := _compiled(q)) is not None:
+        out = serve.fwd(q, pool, page_table, start, count, o, lse, workspace, scale, causal, o_fp32)
+        if out is not None:
+            if isinstance(out, int):
+                raise FAError(out, "fa_fwd_kv4")
+            return out
     torch = _torch()
     _check_bhnd("q", q)
     B, H, T, d = q.shape

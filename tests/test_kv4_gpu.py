@@ -671,3 +671,68 @@ def test_a_withheld_arrival_ends_with_a_status(wide):
         fa.fa_debug_set_wait_limit_ms(1000)
     c.check_attention(q, [2099, 900])
     _ok()
+
+
+@pytest.mark.parametrize("compiled", [True, False])
+def test_both_bindings_do_the_same(compiled, monkeypatch):
+    """The compiled binding and the package's own path: results, what is allocated, what is handed back."""
+    if not compiled:
+        monkeypatch.setattr(fa, "_compiled", lambda t: None)
+    else:
+        assert fa._compiled(torch.empty(1, device="cuda")) is not None
+    c = Cache(3, 2, 64, "fp16", 16, 200, seed=32)
+    c.write([0, 0, 0], 100)
+    c.write([100, 0, 7], 20, count=[20, 3, 0])
+    c.check_read([0, 0, 0], 120, count=[120, 100, 100])
+    c.check_read([0, 1, 2], 90)
+    q = _rows(c.g, "fp16", 3, 4, 2, 64)
+    o, lse = c.check_attention(q, [60, 50, 98])
+    assert o.dtype == torch.float16 and o.shape == q.shape and lse.shape == (3, 4, 2)
+    o, _ = c.check_attention(q, [60, 50, 98], o_fp32=True, causal=False, count=[2, 1, 0], scale=0.25)
+    assert o.dtype == torch.float32
+    mine = torch.full((3, 4, 2, 64), 7.0, device="cuda"), torch.empty((3, 4, 2), device="cuda")
+    ws = torch.empty(fa.fa_fwd_kv4_workspace_size(3, 4, 2, 2, 64), dtype=torch.uint8, device="cuda")
+    got = fa.fa_fwd_kv4(q.cuda(), c.pool, c.table, _ints([60, 50, 98]), o=mine[0], lse=mine[1], workspace=ws, scale=1)
+    assert got[0] is mine[0] and got[1] is mine[1]
+    check(c, q, *got, [60, 50, 98], [2, 2, 2], False, 1.0)
+    k, v = fa.fa_kv4_read(c.pool, c.table, _ints([5, 5, 5]), N=1, dtype=torch.float16)
+    assert k.shape == v.shape == (3, 2, 1, 64) and k.data_ptr() != v.data_ptr()
+    _ok()
+
+
+@pytest.mark.parametrize("compiled", [True, False])
+def test_both_bindings_refuse_the_same(compiled, monkeypatch):
+    if not compiled:
+        monkeypatch.setattr(fa, "_compiled", lambda t: None)
+    c = Cache(2, 2, 64, "bf16", 16, 32, seed=33)
+    k = _rows(c.g, "bf16", 2, 2, 3, 64).cuda()
+    s = _ints([0, 0])
+    bad = [(k, k.transpose(2, 3), c.pool, c.table, s), (k.float(), k.float(), c.pool, c.table, s), (k, k.half(), c.pool, c.table, s),
+           (k, k[:1], c.pool, c.table, s), (k.cpu(), k, c.pool, c.table, s), (k, k, c.pool[:, :1], c.table, s),
+           (k, k, c.pool.float(), c.table, s), (k, k, c.pool, c.table.long(), s), (k, k, c.pool, c.table[:1], s),
+           (k, k, c.pool, c.table, s.long()), (k, k, c.pool, c.table, _ints([0])), (k, k, c.pool, c.table, s.cpu()),
+           (k, k, c.pool, c.table.t(), s)]
+    for args in bad:
+        with pytest.raises((ValueError, TypeError)):
+            fa.fa_kv4_write(*args)
+        with pytest.raises((ValueError, TypeError, fa.FAError)):
+            if args[1] is k or args[0].dtype == torch.float32:
+                fa.fa_fwd_kv4(args[0], *args[2:])
+            else:
+                raise ValueError
+    for kw in (dict(o=torch.empty(2, 2, 3, 64, device="cuda", dtype=torch.float64)), dict(lse=torch.empty(2, 2, 4, device="cuda")),
+               dict(workspace=torch.empty(1 << 25, dtype=torch.uint8)), dict(o=torch.empty(2, 2, 3, 64))):
+        with pytest.raises(ValueError):
+            fa.fa_fwd_kv4(k, c.pool, c.table, s, **kw)
+    with pytest.raises(fa.FAError, match="WORKSPACE"):
+        fa.fa_fwd_kv4(k, c.pool, c.table, s, workspace=torch.empty(16, dtype=torch.uint8, device="cuda"))
+    with pytest.raises(fa.FAError, match="INVALID"):
+        fa.fa_fwd_kv4(k, c.pool, c.table, s, scale=-1.0)
+    with pytest.raises(fa.FAError, match="INVALID"):
+        fa.fa_fwd_kv4(torch.cat([k, k[:, :1]], 1)[:, :0].contiguous(), c.pool, c.table, s)
+    for n, t in ((None, torch.bfloat16), (4, torch.float32), (4, None)):
+        with pytest.raises(ValueError):
+            fa.fa_kv4_read(c.pool, c.table, s, N=n, dtype=t)
+    with pytest.raises((RuntimeError, fa.FAError)):
+        fa.fa_kv4_read(c.pool, c.table, s, N=0, dtype=torch.bfloat16)
+    _ok()
