@@ -352,10 +352,8 @@ __global__ void __launch_bounds__(kThreads, (Shape<D, NT, C>::CtasPerSm)) fa_kv4
     for (int i = threadIdx.x; i < kSeen && b_seen + i < p.B; i += kThreads)
       seen[i] = make_int2(p.c.start[b_seen + i], kv4_count(p.c, b_seen + i, p.T));
     __syncthreads();
-    if (lo >= hi) {
-      if (lane == 0 && !p.join_units) p.joins[worker].parts = 0;
-      return;
-    }
+    if (lane == 0 && !p.join_units) p.joins[worker].parts = 0;   // unless a unit goes on behind the range
+    if (lo >= hi) return;
     left = (int)(hi - lo);
     long long rem = lo - first_sum;   // steps behind the first one of sequence at.b
     at.b = first * per;
@@ -417,7 +415,6 @@ __global__ void __launch_bounds__(kThreads, (Shape<D, NT, C>::CtasPerSm)) fa_kv4
 
   const bool no_steps = left == 0;
   const WaitCtx wc{p.wait_limit_ns, &abort_flag, p.c.status};
-  Kv4Join join{0, 0, 0, 0};
   const int group = p.H / p.c.Hkv;
   const long long unit_rows = (long long)group * p.T;
   uint32_t exist = 0;                          // as `have`, from the step to come on
@@ -794,14 +791,9 @@ __global__ void __launch_bounds__(kThreads, (Shape<D, NT, C>::CtasPerSm)) fa_kv4
             p.lse[row0 + row] = (m[nt][c] + log2f(ll)) * 0.69314718055994531f;
         }
       }
-    if (!Near && begins) {
-      const Kv4Join mine{row0, rows, (int)worker, (int)((r.steps - s1 + each - 1) / each)};
-      if (p.join_units) {
-        if (lane == 0) p.joins[unit] = mine;
-      } else if (!ends) {
-        join = mine;
-      }
-    }
+    if (!Near && begins && lane == 0 && (p.join_units || !ends))
+      p.joins[p.join_units ? unit : worker] =
+          Kv4Join{row0, rows, (int)worker, (int)((r.steps - s1 + each - 1) / each)};
     at_step = 0;
     move_on(at, r);
   }
@@ -812,9 +804,7 @@ __global__ void __launch_bounds__(kThreads, (Shape<D, NT, C>::CtasPerSm)) fa_kv4
       phase ^= slot == ST - 1;
       slot = slot == ST - 1 ? 0 : slot + 1;
     }
-    join.parts = 0;
   }
-  if (!Near && lane == 0 && !p.join_units) p.joins[worker] = join;
   if constexpr (Near) {
     if (no_steps || !alive) {   // an empty piece
       float* const part = reinterpret_cast<float*>(ring);
