@@ -258,7 +258,7 @@ __global__ void __launch_bounds__(kThreads, (Shape<D, NT, C>::CtasPerSm)) fa_kv4
   constexpr int kBatch = 32 / KB;   // steps whose pages a warp looks up at once
   extern __shared__ __align__(128) uint8_t ring_all[];
   __shared__ __align__(8) uint64_t bars[kWarps][ST];
-  __shared__ long long warp_sum[kWarps];
+  __shared__ long long warp_sum[kWarps], split[2];
   __shared__ int abort_flag;
   __shared__ int2 seen[kSeen];   // start and count
   long long* const chunk_sum = reinterpret_cast<long long*>(ring_all);   // until the first copies
@@ -299,7 +299,6 @@ __global__ void __launch_bounds__(kThreads, (Shape<D, NT, C>::CtasPerSm)) fa_kv4
 
   // ---- which steps are this warp's
   const long long worker = (long long)blockIdx.x * kWarps + warp;
-  long long each = 0;
   int left = 0;   // steps (2^31 of them would be hours)
   Place at{0, 0, 0};   // the unit at hand
   int at_step = 0;     // and the step in it that comes next
@@ -337,8 +336,11 @@ __global__ void __launch_bounds__(kThreads, (Shape<D, NT, C>::CtasPerSm)) fa_kv4
     chunk_sum[threadIdx.x] = before + incl - mine;
     __syncthreads();
 
-    each = (total + p.workers - 1) / p.workers;
-    const long long lo = worker * each, hi = lo + each < total ? lo + each : total;
+    const long long workers = total < p.workers ? total : p.workers;
+    const long long each = total / workers, more = total - each * workers;   // the first `more` have one step more
+    auto begin_of = [&](long long w) { return w < workers ? w * each + (w < more ? w : more) : total; };
+    const long long here = begin_of(worker);
+    if (threadIdx.x == 0) split[0] = each, split[1] = more;
     // the last chunk of sequences that does not begin behind a step
     auto chunk_of = [&](long long step) {
       int n = 0;
@@ -346,16 +348,16 @@ __global__ void __launch_bounds__(kThreads, (Shape<D, NT, C>::CtasPerSm)) fa_kv4
       for (int i = 0; i < kThreads / 32; ++i) n += __popc(__ballot_sync(0xffffffffu, chunk_sum[32 * i + lane] <= step));
       return n - 1;
     };
-    const int first = chunk_of(lo);
-    b_seen = chunk_of(lo - warp * each) * per;
+    const int first = chunk_of(here);
+    b_seen = chunk_of(begin_of(worker - warp)) * per;
     const long long first_sum = chunk_sum[first];
     for (int i = threadIdx.x; i < kSeen && b_seen + i < p.B; i += kThreads)
       seen[i] = make_int2(p.c.start[b_seen + i], kv4_count(p.c, b_seen + i, p.T));
     __syncthreads();
     if (lane == 0 && !p.join_units) p.joins[worker].parts = 0;   // unless a unit goes on behind the range
-    if (lo >= hi) return;
-    left = (int)(hi - lo);
-    long long rem = lo - first_sum;   // steps behind the first one of sequence at.b
+    left = (int)(begin_of(worker + 1) - here);
+    if (left == 0) return;
+    long long rem = here - first_sum;   // steps behind the first one of sequence at.b
     at.b = first * per;
     Reach r = reach(at.b);
     while (rem >= r.steps * p.units_per_seq) {
@@ -791,9 +793,16 @@ __global__ void __launch_bounds__(kThreads, (Shape<D, NT, C>::CtasPerSm)) fa_kv4
             p.lse[row0 + row] = (m[nt][c] + log2f(ll)) * 0.69314718055994531f;
         }
       }
-    if (!Near && begins && lane == 0 && (p.join_units || !ends))
-      p.joins[p.join_units ? unit : worker] =
-          Kv4Join{row0, rows, (int)worker, (int)((r.steps - s1 + each - 1) / each)};
+    if (!Near && begins && lane == 0 && (p.join_units || !ends)) {
+      int parts = 0;
+      if (!ends) {   // then this worker's range ends here, and the unit's last step lies behind it
+        const long long each = split[0], more = split[1];
+        const long long last = (worker + 1) * each + (worker + 1 < more ? worker + 1 : more) + (r.steps - s1) - 1;
+        const long long more_end = more * (each + 1);
+        parts = (int)((last < more_end ? last / (each + 1) : more + (last - more_end) / each) - worker);
+      }
+      p.joins[p.join_units ? unit : worker] = Kv4Join{row0, rows, (int)worker, parts};
+    }
     at_step = 0;
     move_on(at, r);
   }
