@@ -43,7 +43,7 @@
 // for 16 keys; with 12 warps a SM that is about 90 SM cycles where memory
 // needs 100, and the two overlap.  Measured on B200 (graph of calls): 8
 // sequences of 65536 keys and 8 rows 115 us, 5.3 TB/s; 64 sequences of up to
-// 8192 keys and 4 rows 73 us, 4.5 TB/s, about 15 us of both being the
+// 8192 keys and 4 rows 68 us, 4.8 TB/s, about 14 us of both being the
 // start, the ends of units and the joining kernel; one sequence of 1000 keys
 // 8.0 us.  A product costs its pipe 8.5 cycles a SM quarter and delays the
 // integer instructions beside it (4 of them and 4 half-precision ones: 12.8),
@@ -883,11 +883,12 @@ __global__ void __launch_bounds__(kJoinThreads) fa_kv4_join_kernel(const Kv4FwdP
 }
 
 constexpr int kMaxSms = 160;
-// Most steps a warp for which a cluster a unit is the better division: 8 key
+// Most keys a warp for which a cluster a unit is the better division: 8 key
 // heads of one sequence, d = 128, four query heads each, take 13.4 us over 8192
-// keys (4 steps) and 18.5 over 16384 (8), the other division 19.6 and 22.4; of
-// four sequences over 16384 keys it takes 27.8 where clusters take 29.6.
-constexpr int kNear = 8;
+// keys (256 a warp) and 18.5 over 16384 (512), the other division 19.6 and
+// 22.4; 16 sequences of up to 9000 keys take 28.2 us in the other division and
+// would take 33.7 in clusters (600).
+constexpr int kNear = 512;
 
 // Lets a kernel have its dynamic shared memory, once per device.
 template <typename Kernel>
@@ -912,12 +913,16 @@ cudaError_t launch(Kv4FwdParams p, void* workspace, int sms, cudaStream_t st) {
   p.units_per_seq = (long long)p.c.Hkv * p.row_tiles;
   const long long units = p.B * p.units_per_seq;
 
-  // Few and short units: a cluster each.  The largest cluster that finds room at
-  // once and has a step for each warp, while no warp gets more than kNear.
+  // Few and short units: a cluster each.  The largest cluster that has a step
+  // for each warp and leaves an eighth of the GPU's places free (a cluster's
+  // CTAs lie in one of its parts, so the last places do not fill: 144 units of
+  // 1000 keys, d = 64, take 10.0 us in clusters of 3 and 14.0 in clusters of 4),
+  // while no warp gets more than kNear keys.
   const long long most = (((long long)p.c.max_pages << p.c.page_shift) + Sh::Step - 1) / Sh::Step;   // steps of a unit
+  const long long places = (long long)sms * Sh::CtasPerSm * 7 / 8;
   int cluster = 8;
-  while (cluster > 1 && (units * cluster > (long long)sms * Sh::CtasPerSm || cluster / 2 * kWarps >= most)) cluster /= 2;
-  if (units * cluster <= (long long)sms * Sh::CtasPerSm && most <= (long long)cluster * kWarps * kNear) {
+  while (cluster > 1 && (units * cluster > places || (cluster - 1) * kWarps >= most)) --cluster;
+  if (units * cluster <= places && most <= (long long)cluster * kWarps * (kNear / Sh::Step)) {
     p.cluster = cluster;
     auto kern = fa_kv4_fwd_kernel<BF16, D, NT, C, true>;
     if ((e = prepare(kern, Sh::Smem, &near_done)) != cudaSuccess) return e;
@@ -947,7 +952,7 @@ cudaError_t launch(Kv4FwdParams p, void* workspace, int sms, cudaStream_t st) {
 
 // Query rows that share a key head go in tiles of 8 columns.  One row in two
 // columns where four rows share a head: 64 sequences of up to 8192 keys, d =
-// 128, 73.7 us against 77.7.  Two tiles a unit where more than 8 rows do: 64
+// 128, took 73.7 us against 77.7.  Two tiles a unit where more than 8 rows do: 64
 // sequences of 4096 keys and 12 rows, 106 us against 119 with one.  (Four,
 // where registers allow them at d = 64, lost: 18.4 against 14.8 us for two
 // sequences of 3000 keys and 384 rows a head.)
