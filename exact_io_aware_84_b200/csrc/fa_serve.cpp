@@ -91,6 +91,7 @@ struct Cache {
 
 void* current_stream(int dev) { return c10::cuda::getCurrentCUDAStream((c10::DeviceIndex)dev).stream(); }
 
+// f() must not throw: pointers and streams are looked up before.
 template <typename F>
 int without_gil(F&& f) {
   int st;
@@ -108,9 +109,11 @@ PyObject* serve_write(PyObject*, PyObject* const* a, Py_ssize_t n) {
   if (n != 6 || !k.take(a[0]) || !v.take(a[1]) || !c.take(a[2], a[3], a[4], a[5], k.dev)) Py_RETURN_NONE;
   if (v.t->sizes() != k.t->sizes() || v.dtype != k.dtype) Py_RETURN_NONE;
   if (c.B != k.B || c.heads != k.heads || c.d != k.d) Py_RETURN_NONE;
+  const void *pk = k.t->data_ptr(), *pv = v.t->data_ptr();
+  void* const stream = current_stream(k.dev);
   return PyLong_FromLong(without_gil([&] {
-    return g_write(k.t->data_ptr(), v.t->data_ptr(), c.pool, c.table, c.start, c.count, k.B, k.heads, k.rows, k.d,
-                   c.n_pages, c.page, c.max_pages, k.dtype, current_stream(k.dev));
+    return g_write(pk, pv, c.pool, c.table, c.start, c.count, k.B, k.heads, k.rows, k.d, c.n_pages, c.page,
+                   c.max_pages, k.dtype, stream);
   }));
   END_HANDLE_TH_ERRORS
 }
@@ -127,14 +130,13 @@ PyObject* serve_read(PyObject*, PyObject* const* a, Py_ssize_t n) {
   if (over != 0 || rows <= 0 || !fits(rows) || (type != at::kBFloat16 && type != at::kHalf)) Py_RETURN_NONE;
   const auto options = at::TensorOptions().dtype(type).device(at::kCUDA, (c10::DeviceIndex)dev);
   const at::Tensor k = at::empty({c.B, c.heads, rows, c.d}, options), v = at::empty({c.B, c.heads, rows, c.d}, options);
+  void *const pk = k.data_ptr(), *const pv = v.data_ptr(), *const stream = current_stream(dev);
   const int st = without_gil([&] {
-    return g_read(c.pool, c.table, c.start, c.count, k.data_ptr(), v.data_ptr(), c.B, c.heads, (int)rows, c.d,
-                  c.n_pages, c.page, c.max_pages, type == at::kBFloat16 ? FA_BF16 : FA_FP16, current_stream(dev));
+    return g_read(c.pool, c.table, c.start, c.count, pk, pv, c.B, c.heads, (int)rows, c.d, c.n_pages, c.page,
+                  c.max_pages, type == at::kBFloat16 ? FA_BF16 : FA_FP16, stream);
   });
   if (st != FA_OK) return PyLong_FromLong(st);
-  PyObject* pk = THPVariable_Wrap(k);
-  PyObject* pv = THPVariable_Wrap(v);
-  return Py_BuildValue("(NN)", pk, pv);
+  return Py_BuildValue("(NN)", THPVariable_Wrap(k), THPVariable_Wrap(v));
   END_HANDLE_TH_ERRORS
 }
 
@@ -184,15 +186,17 @@ PyObject* serve_fwd(PyObject*, PyObject* const* a, Py_ssize_t n) {
   }
   const bool o32 = o->scalar_type() == at::kFloat;
   const int dtype = q.dtype == FA_BF16 ? (o32 ? FA_BF16_O_F32 : FA_BF16) : (o32 ? FA_FP16_O_F32 : FA_FP16);
+  const void* const pq = q.t->data_ptr();
+  void *const po = o->data_ptr(), *const pl = lse->data_ptr(), *const pw = ws->data_ptr();
+  void* const stream = current_stream(q.dev);
+  const size_t ws_bytes = ws->nbytes();
   const int st = without_gil([&] {
-    return g_fwd(q.t->data_ptr(), c.pool, c.table, c.start, c.count, o->data_ptr(),
-                 static_cast<float*>(lse->data_ptr()), ws->data_ptr(), ws->nbytes(), q.B, q.heads, c.heads, q.rows,
-                 q.d, c.n_pages, c.page, c.max_pages, (float)scale, causal, dtype, current_stream(q.dev));
+    return g_fwd(pq, c.pool, c.table, c.start, c.count, po, static_cast<float*>(pl), pw, ws_bytes, q.B, q.heads,
+                 c.heads, q.rows, q.d, c.n_pages, c.page, c.max_pages, (float)scale, causal, dtype, stream);
   });
   if (st != FA_OK) return PyLong_FromLong(st);
-  PyObject* po = a[5] != Py_None ? Py_NewRef(a[5]) : THPVariable_Wrap(new_o);
-  PyObject* pl = a[6] != Py_None ? Py_NewRef(a[6]) : THPVariable_Wrap(new_lse);
-  return Py_BuildValue("(NN)", po, pl);
+  return Py_BuildValue("(NN)", a[5] != Py_None ? Py_NewRef(a[5]) : THPVariable_Wrap(new_o),
+                       a[6] != Py_None ? Py_NewRef(a[6]) : THPVariable_Wrap(new_lse));
   END_HANDLE_TH_ERRORS
 }
 
