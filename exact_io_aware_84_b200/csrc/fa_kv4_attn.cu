@@ -71,7 +71,7 @@ namespace {
 
 constexpr int kWarps = 4;               // of a CTA
 constexpr int kThreads = 32 * kWarps;
-constexpr int kSeen = 128;              // sequences whose lengths a CTA keeps at hand
+constexpr int kSeen = kThreads;         // sequences whose lengths a CTA keeps at hand
 constexpr float kUnit = 16777216.f;     // scores and O are summed in units of 2^-24, the subnormals' step
 constexpr float kLeast = -3.402823466e38f;   // a maximum before the first key
 constexpr float kVPass = 128.f;              // with P below 2^8, P s_V stays in fp16's range
@@ -314,7 +314,9 @@ __global__ void __launch_bounds__(kThreads, (Shape<D, NT, C>::CtasPerSm)) fa_kv4
     const int per = (p.B + kThreads - 1) / kThreads;
     long long mine = 0;
     for (int i = 0, b = threadIdx.x * per; i < per && b < p.B; ++i, ++b) {
-      const Reach r(p, p.c.start[b], kv4_count(p.c, b, p.T), Sh::Step);
+      const int2 x = make_int2(p.c.start[b], kv4_count(p.c, b, p.T));
+      const Reach r(p, x.x, x.y, Sh::Step);
+      if (per == 1) seen[threadIdx.x] = x;
       mine += r.steps;
       if (blockIdx.x == 0) past_table(r);
     }
@@ -349,10 +351,12 @@ __global__ void __launch_bounds__(kThreads, (Shape<D, NT, C>::CtasPerSm)) fa_kv4
       return n - 1;
     };
     const int first = chunk_of(here);
-    b_seen = chunk_of(begin_of(worker - warp)) * per;
     const long long first_sum = chunk_sum[first];
-    for (int i = threadIdx.x; i < kSeen && b_seen + i < p.B; i += kThreads)
-      seen[i] = make_int2(p.c.start[b_seen + i], kv4_count(p.c, b_seen + i, p.T));
+    if (per > 1) {   // not all of them fit: from the CTA's first one on
+      b_seen = chunk_of(begin_of(worker - warp)) * per;
+      for (int i = threadIdx.x; i < kSeen && b_seen + i < p.B; i += kThreads)
+        seen[i] = make_int2(p.c.start[b_seen + i], kv4_count(p.c, b_seen + i, p.T));
+    }
     __syncthreads();
     if (lane == 0 && !p.join_units) p.joins[worker].parts = 0;   // unless a unit goes on behind the range
     left = (int)(begin_of(worker + 1) - here);
