@@ -565,34 +565,28 @@ __global__ void __launch_bounds__(kThreads, (Shape<D, NT, C>::CtasPerSm)) fa_kv4
 #pragma unroll
             for (int e = 0; e < W / 2; ++e) top2 = max_abs2<BF16>(top2, raw[W / 2 + e]);
           }
-          // the groups' products side by side, so that none waits for another
-          float d[NT][W][4];
 #pragma unroll
           for (int e = 0; e < W; ++e) {
+            float d[NT][4];
             const uint32_t x0 = kw[0][e], x1 = kw[1][e];
-            const uint32_t a[4] = {x0 & 0x000f000fu, x1 & 0x000f000fu, x0 & 0x00f000f0u, x1 & 0x00f000f0u};
+            const uint32_t a0[4] = {x0 & 0x000f000fu, x1 & 0x000f000fu, x0 & 0x00f000f0u, x1 & 0x00f000f0u};
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt) {
               const float4 c = less[4 * (nt * W + e)];
               const float c4[4] = {c.x, c.y, c.z, c.w};
-              mma16816(d[nt][e], a, qb[nt][e][0], qb[nt][e][1], c4);
+              mma16816(d[nt], a0, qb[nt][e][0], qb[nt][e][1], c4);
             }
-          }
-#pragma unroll
-          for (int e = 0; e < W; ++e) {
-            const uint32_t y0 = __byte_perm(kw[0][e], 0, 0x4341), y1 = __byte_perm(kw[1][e], 0, 0x4341);
+            const uint32_t y0 = __byte_perm(x0, 0, 0x4341), y1 = __byte_perm(x1, 0, 0x4341);
             const uint32_t z0 = y0 & 0x00f000f0u, z1 = y1 & 0x00f000f0u;
-            const uint32_t a[4] = {hsub2(y0, z0), hsub2(y1, z1), z0, z1};
+            const uint32_t a1[4] = {hsub2(y0, z0), hsub2(y1, z1), z0, z1};
 #pragma unroll
-            for (int nt = 0; nt < NT; ++nt) mma16816(d[nt][e], a, qb[nt][e][2], qb[nt][e][3], d[nt][e]);
-          }
+            for (int nt = 0; nt < NT; ++nt) mma16816(d[nt], a1, qb[nt][e][2], qb[nt][e][3], d[nt]);
 #pragma unroll
-          for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-            for (int e = 0; e < W; ++e)
+            for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
               for (int i = 0; i < 4; ++i)
-                sc[nt][bk][i] = e == 0 ? d[nt][e][i] * sk[i / 2][0] : fmaf(d[nt][e][i], sk[i / 2][e], sc[nt][bk][i]);
+                sc[nt][bk][i] = e == 0 ? d[nt][i] * sk[i / 2][0] : fmaf(d[nt][i], sk[i / 2][e], sc[nt][bk][i]);
+          }
         }
         if (which != (1u << KB) - 1 || key0 + Sh::Step > full_end) {
           // keys that a row does not see; V's scales behind the last key may be
