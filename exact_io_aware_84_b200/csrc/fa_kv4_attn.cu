@@ -42,7 +42,7 @@
 // d = 128 and up to 8 rows a warp issues about 240 instructions and 16 products
 // for 16 keys; with 12 warps a SM that is about 90 SM cycles where memory
 // needs 100, and the two overlap.  Measured on B200 (graph of calls): 8
-// sequences of 65536 keys and 8 rows 115 us, 5.3 TB/s; 64 sequences of up to
+// sequences of 65536 keys and 8 rows 112 us, 5.4 TB/s; 64 sequences of up to
 // 8192 keys and 4 rows 68 us, 4.8 TB/s, about 14 us of both being the
 // start, the ends of units and the joining kernel; one sequence of 1000 keys
 // 8.0 us.  A product costs its pipe 8.5 cycles a SM quarter and delays the
