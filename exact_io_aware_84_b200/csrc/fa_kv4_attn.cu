@@ -357,6 +357,7 @@ __global__ void __launch_bounds__(kThreads, (Shape<D, NT, C>::CtasPerSm)) fa_kv4
       for (int i = threadIdx.x; i < kSeen && b_seen + i < p.B; i += kThreads)
         seen[i] = make_int2(p.c.start[b_seen + i], kv4_count(p.c, b_seen + i, p.T));
     }
+    fence_async_smem();   // the first copies go where chunk_sum was
     __syncthreads();
     if (lane == 0 && !p.join_units) p.joins[worker].parts = 0;   // unless a unit goes on behind the range
     left = (int)(begin_of(worker + 1) - here);
