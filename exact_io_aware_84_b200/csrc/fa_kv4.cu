@@ -53,9 +53,11 @@ __device__ __forceinline__ uint32_t min2_nan(uint32_t a, uint32_t b) {
   return r;
 }
 
+// All lanes of a warp together: volatile, so that it stays where the source
+// has the warp whole.
 __device__ __forceinline__ uint32_t transpose8x8(uint32_t x) {
   uint32_t r;
-  asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(x));
+  asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(x));
   return r;
 }
 
@@ -217,6 +219,7 @@ __global__ void __launch_bounds__(kThreads) fa_kv4_write_kernel(const WriteParam
       const uint16_t s = quantise4<BF16>(x4, w4, lane);
       if (mine) reinterpret_cast<uint16_t*>(blk + 16 * D)[(half * 8 + g) * 2 * W + 4 * q + t] = s;
     }
+    __syncwarp();
 #pragma unroll
     for (int e = 0; e < W; ++e) word[W + e] = transpose8x8(word[W + e]);   // lane: r = g, keys 2t and 2t + 1
     uint32_t* const kw = reinterpret_cast<uint32_t*>(blk) + (half * 32 + lane) * W;
@@ -304,12 +307,15 @@ __global__ void __launch_bounds__(kThreads) fa_kv4_read_kernel(const ReadParams 
       }
     }
   }
+  __syncwarp();
+#pragma unroll
+  for (int half = 0; half < 2; ++half)
+#pragma unroll
+    for (int e = 0; e < W; ++e) vw[half][e] = transpose8x8(vw[half][e]);
 #pragma unroll
   for (int half = 0; half < 2; ++half) {
     const long long row = first + half * 8 + g;
     const bool live = blk != nullptr && row < r.n;
-#pragma unroll
-    for (int e = 0; e < W; ++e) vw[half][e] = transpose8x8(vw[half][e]);
     if (row < 0 || row >= p.N) continue;
 #pragma unroll
     for (int e = 0; e < W; ++e) {

@@ -90,3 +90,36 @@ def test_first_copies_after_the_plan(B):
         o2, lse2 = fa.fa_fwd_kv4(q, c.pool, c.table, s, causal=True)
         assert torch.equal(o, o2) and torch.equal(lse, lse2)
     _ok()
+
+
+# ---------------------------------------------------------------- writing and reading parts of a block
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp16"])
+@pytest.mark.parametrize("d", [64, 128])
+def test_every_part_of_a_block_is_written_and_read(d, dtype):
+    """Some lanes of a warp have rows to write or read, others none: every first position and length within two blocks,
+    a sequence each."""
+    part = [(at, n) for at in range(16) for n in range(1, 18)]
+    B = len(part)
+    c = Cache(B, 1, d, dtype, 16, 33, seed=d)
+    c.write([0] * B, 33)
+    c.check_read([0] * B, 33)
+    start, count = [at for at, _ in part], [n for _, n in part]
+    c.write(start, 17, count=count)
+    c.check_read([0] * B, 33)
+    c.check_read(start, 17, count=count)
+    _ok()
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp16"])
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("n", [1, 2, 7, 8, 9, 15, 16, 17])
+def test_rows_end_anywhere_in_a_block(n, d, dtype):
+    c = Cache(16, 2, d, dtype, 16, 33, seed=n + d)
+    c.write([0] * 16, 33)
+    c.check_read(list(range(16)), n)
+    c.write(list(range(16)), n)
+    c.check_read(list(range(16)), n)
+    c.check_read([0] * 16, 33)
+    _ok()
