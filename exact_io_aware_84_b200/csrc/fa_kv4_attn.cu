@@ -30,13 +30,24 @@
 //   O^T = V^T P^T: the head's elements as rows.  V's codes become n by one
 //     fp16 subtraction, exactly: a sum over many keys must not carry an offset
 //     (taking it back by a product with -8 measured 6% slower).  P s_V is
-//     rounded to fp16, with s_V taken relative to the largest one so far (a
-//     power of two, which O's end takes back), and changes from accumulator to
-//     operand order by movmatrix.  A product's rows belong to one group of 32
-//     elements, as s_V does; with C > 1 they belong to two, and a row's columns
-//     hold P s_V for one group each, so that C times fewer are made.
-// The running maximum moves only when a score passes it by 2^8: P stays below
-// 2^8 and P s_V below 2^15.
+//     rounded to fp16 after a factor v_up of its row, which O's end takes back,
+//     and changes from accumulator to operand order by movmatrix.  A product's
+//     rows belong to one group of 32 elements, as s_V does; with C > 1 they
+//     belong to two, and a row's columns hold P s_V for one group each, so that
+//     C times fewer are made.
+// The running maximum m moves only when a score passes it by 2^8: P stays below
+// 2^8.  v_up follows the row's largest P |s_V| so far in the same way: it falls,
+// bringing that to 2^6 .. 2^7, when a bound on the step's passes 2^15, and it
+// rises as m does, so that what O's sums are relative to does not change with
+// m.  A row thus rounds relative to the products of the keys that it sees: keys
+// of other rows, and keys of no weight whatever their values, have no say.  The
+// bound is the largest P of a lane's keys times the largest |s_V| of any key of
+// theirs; the products themselves are looked at where it passes.  (A factor
+// common to a tile's rows and taken from V's scales alone was 2 to 5% faster and
+// lost rows beside a key of large V that they did not see.)  P s_V in fp16 adds
+// 2^-11 a term to an error that O's own rounding to fp16 bounds by 2^-11 (2.1e-4
+// to 2.9e-4 over 24 x 4 tokens of 128); two halves of P s_V would double the
+// products, of which a step has as many for V as for K.
 //
 // What bounds it.  Reading the cache once: 9D/8 bytes a key and key head.  At
 // d = 128 and up to 8 rows a warp issues about 240 instructions and 16 products
@@ -74,8 +85,8 @@ constexpr int kThreads = 32 * kWarps;
 constexpr int kSeen = kThreads;         // sequences whose lengths a CTA keeps at hand
 constexpr float kUnit = 16777216.f;     // scores and O are summed in units of 2^-24, the subnormals' step
 constexpr float kLeast = -3.402823466e38f;   // a maximum before the first key
-constexpr float kVPass = 128.f;              // with P below 2^8, P s_V stays in fp16's range
-constexpr int kMostUp = 106;                 // P v_up stays finite
+constexpr float kVPass = 32768.f, kVPassLog2 = 15.f;   // P s_V stays in fp16's range
+constexpr float kMostUp = 0x1p118f;          // P v_up stays finite
 constexpr float kLazy = 8.f;            // log2 by which a score may pass the running maximum
 
 template <int D, int NT, int C>
@@ -158,6 +169,12 @@ __device__ __forceinline__ float quad_sum(float x) {
   x += __shfl_xor_sync(0xffffffffu, x, 4);
   x += __shfl_xor_sync(0xffffffffu, x, 8);
   return x + __shfl_xor_sync(0xffffffffu, x, 16);
+}
+
+__device__ __forceinline__ float lg2_approx(float x) {
+  float r;
+  asm("lg2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+  return r;
 }
 
 __device__ __forceinline__ float pow2(int e) { return __int_as_float((e + 127) << 23); }   // -126 <= e <= 127
@@ -514,6 +531,7 @@ __global__ void __launch_bounds__(kThreads, (Shape<D, NT, C>::CtasPerSm)) fa_kv4
     last_key = __reduce_max_sync(0xffffffffu, last_key);
 
     float o[NT][W][2][4], m[NT][2], l[NT][2];
+    float v_up[NT][2];   // P s_V goes in times v_up, up to kVPass
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
 #pragma unroll
@@ -521,9 +539,8 @@ __global__ void __launch_bounds__(kThreads, (Shape<D, NT, C>::CtasPerSm)) fa_kv4
 #pragma unroll
         for (int i = 0; i < 8; ++i) o[nt][e][i / 4][i % 4] = 0.f;
 #pragma unroll
-      for (int c = 0; c < 2; ++c) m[nt][c] = kLeast, l[nt][c] = 0.f;
+      for (int c = 0; c < 2; ++c) m[nt][c] = kLeast, l[nt][c] = 0.f, v_up[nt][c] = kMostUp;
     }
-    float v_up = pow2(kMostUp);   // s_V goes in times v_up, up to kVPass
 
     for (int s = s0; s < s1; ++s, --left) {
       const uint32_t bar = bar0 + 8 * slot;
@@ -616,9 +633,8 @@ __global__ void __launch_bounds__(kThreads, (Shape<D, NT, C>::CtasPerSm)) fa_kv4
           fence_async_smem();   // before the next copy to this stage
           __syncwarp();
         }
-        // ---- V's scales go in relative to the largest so far
         const float v_top = fmaxf(fabsf(kv4_scale<BF16>((uint16_t)top2)), fabsf(kv4_scale<BF16>((uint16_t)(top2 >> 16))));
-        bool pass = v_top * v_up > kVPass;
+        bool pass = false;
         float top[NT][2];
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
@@ -627,34 +643,54 @@ __global__ void __launch_bounds__(kThreads, (Shape<D, NT, C>::CtasPerSm)) fa_kv4
             top[nt][c] = fmaxf(sc[nt][0][c], sc[nt][0][2 + c]);
 #pragma unroll
             for (int bk = 1; bk < KB; ++bk) top[nt][c] = fmax3(top[nt][c], sc[nt][bk][c], sc[nt][bk][2 + c]);
-            pass = pass || fmaf(top[nt][c], f[nt][c], -m[nt][c]) > kLazy;
+            // P <= 2^kLazy and P v_top v_up <= kVPass
+            const float room = fminf(kLazy, kVPassLog2 - lg2_approx(v_top * v_up[nt][c]));
+            pass = pass || fmaf(top[nt][c], f[nt][c], -m[nt][c]) > room;
           }
         if (__any_sync(0xffffffffu, pass)) {
-          float all = v_top;
-#pragma unroll
-          for (int d = 16; d; d /= 2) all = fmaxf(all, __shfl_xor_sync(0xffffffffu, all, d));
-          float fv = 1.f;
-          if (all * v_up > kVPass) {
-            const int ex = 6 + 127 - (int)(__float_as_uint(all) >> 23);   // all * 2^ex in [2^6, 2^7)
-            const float up = pow2(min(ex, kMostUp));
-            fv = up / v_up;
-            v_up = up;
-          }
+          float most[NT][2] = {};   // the row's largest P |s_V| in this step
+          float fo[NT][2];          // what O's sums are multiplied by
 #pragma unroll
           for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
             for (int c = 0; c < 2; ++c) {
               const float best = quad_max(top[nt][c]), mx = f[nt][c] * best;
-              float fm = 1.f;
+              fo[nt][c] = 1.f;
               if (fmaf(best, f[nt][c], -m[nt][c]) > kLazy) {   // as above: no other row has a say in it
-                fm = ex2_approx(m[nt][c] - mx);
+                const float fm = ex2_approx(m[nt][c] - mx), up = fminf(v_up[nt][c] * ex2_approx(mx - m[nt][c]), kMostUp);
+                fo[nt][c] = __fdividef(fm * up, v_up[nt][c]);   // 1, or less where v_up is at its end
+                v_up[nt][c] = up;
                 m[nt][c] = mx;
                 l[nt][c] *= fm;
               }
+            }
+#pragma unroll
+          for (int i = 0; i < 2 * KB; ++i) {
+            const uint32_t* const vs = reinterpret_cast<const uint32_t*>(base + i / 2 * Block + 16 * D) + (i % 2 * 8 + g) * W + W / 2;
+            uint32_t x = vs[0];
+#pragma unroll
+            for (int e = 1; e < W / 2; ++e) x = max_abs2<BF16>(x, vs[e]);
+            const float sv = fmaxf(fabsf(kv4_scale<BF16>((uint16_t)x)), fabsf(kv4_scale<BF16>((uint16_t)(x >> 16))));
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+              for (int c = 0; c < 2; ++c)
+                most[nt][c] = fmaxf(most[nt][c], ex2_approx(fmaf(sc[nt][i / 2][2 * (i % 2) + c], f[nt][c], -m[nt][c])) * sv);
+          }
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+            for (int c = 0; c < 2; ++c) {
+              const float y = quad_max(most[nt][c]);
+              if (y * v_up[nt][c] > kVPass) {
+                const float up = pow2(6 + 127 - (int)(__float_as_uint(y) >> 23));   // y * up in [2^6, 2^7)
+                fo[nt][c] *= __fdividef(up, v_up[nt][c]);
+                v_up[nt][c] = up;
+              }
 #pragma unroll
               for (int i = 0; i < 2 * W; ++i) {
-                o[nt][i / 2][i % 2][c] *= fm * fv;
-                o[nt][i / 2][i % 2][2 + c] *= fm * fv;
+                o[nt][i / 2][i % 2][c] *= fo[nt][c];
+                o[nt][i / 2][i % 2][2 + c] *= fo[nt][c];
               }
             }
         }
@@ -669,7 +705,7 @@ __global__ void __launch_bounds__(kThreads, (Shape<D, NT, C>::CtasPerSm)) fa_kv4
             f2_unpack(f2_fma(f2_pack(x[2 * (i % 2)], x[2 * (i % 2) + 1]), f2_pack(f[nt][0], f[nt][1]), neg), x0, x1);
             const uint64_t pp = f2_pack(ex2_approx(x0), ex2_approx(x1));
             sum = f2_add(sum, pp);
-            f2_unpack(f2_mul(pp, f2_pack(v_up, v_up)), x[2 * (i % 2)], x[2 * (i % 2) + 1]);
+            f2_unpack(f2_mul(pp, f2_pack(v_up[nt][0], v_up[nt][1])), x[2 * (i % 2)], x[2 * (i % 2) + 1]);
           }
           f2_unpack(sum, l[nt][0], l[nt][1]);
         }
@@ -750,7 +786,6 @@ __global__ void __launch_bounds__(kThreads, (Shape<D, NT, C>::CtasPerSm)) fa_kv4
     // ---- the unit's result, or this warp's piece of it
     float* part = begins && ends ? nullptr : slot_of(p, worker, begins ? 1 : 0, Sh::Slot);
     if constexpr (Near) part = reinterpret_cast<float*>(ring);
-    const float v_down = 1.f / v_up;
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
@@ -759,7 +794,7 @@ __global__ void __launch_bounds__(kThreads, (Shape<D, NT, C>::CtasPerSm)) fa_kv4
         float ll = quad_sum(l[nt][c]);
         if (row >= rows) continue;
         if (lim[nt][c] == 0) ll = 0.f;   // steps that all other rows see whole do not mask this one
-        const float even = ll == 0.f ? 0.f : kUnit / ll, odd = even * 0.0625f;
+        const float even = ll == 0.f ? 0.f : kUnit / ll, odd = even * 0.0625f, v_down = __fdividef(1.f, v_up[nt][c]);
 #pragma unroll
         for (int e = 0; e < W; e += C == 1 ? 1 : 2) {
           float4 x;

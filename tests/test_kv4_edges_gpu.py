@@ -123,3 +123,119 @@ def test_rows_end_anywhere_in_a_block(n, d, dtype):
     c.check_read(list(range(16)), n)
     c.check_read([0] * 16, 33)
     _ok()
+
+
+# ---------------------------------------------------------------- values far apart
+
+SHARED = [(1, 1), (2, 1), (4, 2), (4, 1), (8, 1), (24, 2)]   # rows a key head: one column a row, two, four; two tiles; ...
+FAR = [("bf16", 2.0**100), ("bf16", 2.0**30), ("fp16", 60000.0)]
+
+
+@pytest.mark.parametrize("wide", [False, True])
+@pytest.mark.parametrize("dtype,far", FAR)
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("H,Hkv", SHARED)
+def test_a_row_does_not_feel_keys_that_only_later_rows_see(H, Hkv, d, dtype, far, wide):
+    """The last two of three tokens bring values far above all others; small ones all around (fp16: far below 1)."""
+    c = Cache(2, Hkv, d, dtype, 16, 420, seed=H + d)
+    small = 1.0 if dtype == "bf16" else 2.0**-10
+    v = _rows(c.g, dtype, 2, Hkv, 420, d) * small
+    start = [400, 61]
+    for b, at in enumerate(start):
+        v[b, :, at + 1] = far
+        v[b, :, at + 2] = -far
+    c.write([0, 0], 420, v=v)
+    if wide:
+        _room(c)
+    attend(c, _rows(c.g, dtype, 2, H, 3, d), start, o_fp32=True)
+    attend(c, _rows(c.g, dtype, 2, H, 3, d), start, count=[2, 1])
+    _ok()
+
+
+@pytest.mark.parametrize("wide", [False, True])
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("H,T", [(1, 1), (4, 1), (8, 1), (5, 4)])
+def test_a_key_of_no_weight_does_not_matter_whatever_its_value(H, T, d, wide):
+    """One key's value is near the type's largest and its weight e^-200 or less: before, between and behind the others,
+    with the maximum reached before it and after it."""
+    for length, at in ((40, 0), (40, 17), (700, 0), (700, 333), (700, 690), (3000, 5), (3000, 64)):
+        c = Cache(1, 1, d, "bf16", 16, length, seed=length + at)
+        k, v = (_rows(c.g, "bf16", 1, 1, length, d) for _ in range(2))
+        k += 3.0 * 8 / d**0.5
+        k[:, :, at] = -30.0
+        v[:, :, at] = 2.0**126
+        c.write([0], length, k=k, v=v)
+        if wide:
+            _room(c)
+        q = (_rows(c.g, "bf16", 1, H, T, d).float().abs() + 1).bfloat16()
+        attend(c, q, [length - T], o_fp32=True)
+    _ok()
+
+
+@pytest.mark.parametrize("wide", [False, True])
+@pytest.mark.parametrize("dtype", ["bf16", "fp16"])
+@pytest.mark.parametrize("H,d", [(1, 64), (8, 128), (12, 128)])
+def test_a_key_of_all_the_weight_and_no_value_leaves_the_others_exact(H, d, dtype, wide):
+    for at in (0, 250):
+        c = Cache(1, 1, d, dtype, 16, 500, seed=at + H)
+        k, v = (_rows(c.g, dtype, 1, 1, 500, d) for _ in range(2))
+        k *= 0.1
+        k[:, :, at] = 24.0 * 8 / d / d**0.5 * 8          # scores of 1.5 * 24 or so above the others'
+        v[:, :, at] = 0
+        c.write([0], 500, k=k, v=v)
+        if wide:
+            _room(c)
+        q = (_rows(c.g, dtype, 1, H, 1, d).float().abs() * 0.1 + 1).to(TYPES[dtype])
+        attend(c, q, [499], o_fp32=True)
+    _ok()
+
+
+@pytest.mark.parametrize("wide", [False, True])
+@pytest.mark.parametrize("dtype,low,high", [("bf16", -60, 60), ("bf16", -125, 0), ("fp16", -14, 12)])
+def test_magnitudes_along_the_sequence_row_by_row(dtype, low, high, wide):
+    for up in (True, False):
+        c = Cache(1, 1, 64, dtype, 16, 800, seed=int(up))
+        ramp = torch.linspace(low, high, 800) if up else torch.linspace(high, low, 800)
+        v = (torch.randn(1, 1, 800, 64, generator=c.g) * torch.exp2(ramp)[None, None, :, None]).to(TYPES[dtype])
+        c.write([0], 800, v=v)
+        if wide:
+            _room(c)
+        for H, T, at in ((8, 1, 799), (8, 1, 399), (1, 1, 90), (4, 3, 500), (4, 40, 700)):
+            attend(c, _rows(c.g, dtype, 1, H, T, 64), [at], o_fp32=True)
+    _ok()
+
+
+@pytest.mark.parametrize("wide", [False, True])
+def test_results_keep_their_bits_when_the_future_is_written(wide):
+    c = Cache(1, 2, 128, "bf16", 64, 128, seed=17)      # Cache fills the pool with NaN scales
+    if wide:
+        _room(c)
+    c.write([0], 70)
+    q = _rows(c.g, "bf16", 1, 8, 1, 128)
+    before = [attend(c, q, [at]) for at in (69, 68, 40)]
+    big = torch.full((1, 2, 58, 128), torch.finfo(torch.bfloat16).max, dtype=torch.bfloat16)
+    c.write([70], 58, k=big, v=-big)
+    for at, (o, lse) in zip((69, 68, 40), before):
+        o2, lse2 = fa.fa_fwd_kv4(q.cuda(), c.pool, c.table, _ints([at]), causal=True)
+        assert torch.equal(o, o2) and torch.equal(lse, lse2)
+    # the first of two causal rows, the second of which sees one of them
+    q2 = torch.cat([q, q * 2.0**-110], 2)
+    o3, lse3 = fa.fa_fwd_kv4(q2.cuda(), c.pool, c.table, _ints([69]), causal=True)
+    c.k, c.v, c.ks = c.k[:, :, :70], c.v[:, :, :70], c.ks[:, :, :70]
+    strict(c, q, o3[:, :, :1], lse3[:, :, :1], [69])
+    _ok()
+
+
+@pytest.mark.parametrize("wide", [False, True])
+@pytest.mark.parametrize("apart", [12, 20, 24])
+@pytest.mark.parametrize("H,d", [(1, 64), (2, 128), (4, 128), (8, 64), (16, 128)])
+def test_groups_of_one_row_far_apart(H, d, apart, wide):
+    """The first 32 elements of V lie far above the others, which are held to their own size as far as it is promised."""
+    c = Cache(1, 1, d, "bf16", 16, 2000, seed=apart + H)
+    v = _rows(c.g, "bf16", 1, 1, 2000, d)
+    v[..., :32] *= 2.0**apart
+    c.write([0], 2000, v=v)
+    if wide:
+        _room(c)
+    attend(c, _rows(c.g, "bf16", 1, H, 1, d), [1999], o_fp32=True)
+    _ok()
