@@ -192,7 +192,7 @@ __global__ void __launch_bounds__(kThreads) fa_kv4_write_kernel(const WriteParam
   if (u >= p.units) return;
   const Unit r = unit_of(p.c, u, p.blocks, p.T);
   const long long first = r.pos - r.start;         // the block's first token, of this call's
-  if (first >= r.n || first <= -16) return;
+  if (first >= r.n || first <= -16 || r.n == 0) return;
   uint8_t* const blk = kv4_block_of(p.c, r.b, r.h, r.pos, kv4_block_bytes(D));
   if (blk == nullptr) return;
   auto there = [&](int key) { return first + key >= 0 && first + key < r.n; };
@@ -282,7 +282,7 @@ __global__ void __launch_bounds__(kThreads) fa_kv4_read_kernel(const ReadParams 
   const long long first = r.pos - r.start;
   if (first >= p.N || first <= -16) return;
   const uint8_t* blk = nullptr;
-  if (first < r.n) blk = kv4_block_of(p.c, r.b, r.h, r.pos, kv4_block_bytes(D));
+  if (first < r.n && r.n > 0) blk = kv4_block_of(p.c, r.b, r.h, r.pos, kv4_block_bytes(D));
 
   uint32_t kw[2][W], vw[2][W], sw[2][W];   // sw: the scales of a key, two to a word
 #pragma unroll

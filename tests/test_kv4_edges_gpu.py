@@ -16,7 +16,7 @@ import pytest
 import torch
 
 import exact_io_aware_84_b200 as fa
-from oracle import kv4_attn_ref
+from oracle import kv4_attn_ref, round16_ref
 from parity import to64
 from test_kv4_gpu import TYPES, Cache, _ints, _ok, _room, _rows
 
@@ -239,3 +239,28 @@ def test_groups_of_one_row_far_apart(H, d, apart, wide):
         _room(c)
     attend(c, _rows(c.g, "bf16", 1, H, 1, d), [1999], o_fp32=True)
     _ok()
+
+
+# ---------------------------------------------------------------- idle sequences of a padded batch
+
+
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("idle", [0, -5])
+def test_an_idle_sequence_s_pages_are_not_looked_at(idle, d):
+    """Sequences without tokens, whose pages do not exist and whose starts lie inside a block, past the table or before it."""
+    c = Cache(6, 2, d, "bf16", 16, 48, seed=40)
+    c.write([0] * 6, 48)
+    before = c.pool.clone()
+    c.table[1:] = -7
+    start, count = [5, 7, 40, 48 + 9, -3, 2147483647], [3, idle, idle, idle, idle, idle]
+    c.write(start, 3, count=count)
+    _ok()
+    rows = fa.fa_kv4_read(c.pool, c.table, _ints(start), _ints(count), N=20, dtype=torch.bfloat16)
+    _ok()
+    for x, held in zip(rows, (c.k, c.v)):
+        assert not x[1:].any() and not x[0, :, 3:].any()
+        assert np.array_equal(to64(x[0, :, :3]), round16_ref(held[0, :, 5:8], "bf16"))
+    attend(c, _rows(c.g, "bf16", 6, 4, 3, d), start, count=count)
+    _ok()
+    used = (c.pool != before).flatten(1).any(1).nonzero().flatten().tolist()
+    assert used in ([], [int(c.table[0, 0])])
