@@ -26,12 +26,13 @@ struct NvtxRange {
   NvtxRange& operator=(const NvtxRange&) = delete;
 };
 
-// Device status word: 0 = OK, else the fa_status of a kernel that gave up.
-__device__ int g_device_status = 0;
+// Device status: 0 = OK, else FA_ERR_TIMEOUT of a kernel that gave up, and,
+// in a word of its own so that neither hides the other, FA_ERR_PAGE.
+__device__ int g_device_status[2] = {0, 0};
 
 namespace {
 
-// The current device's status word (looked up once per device).
+// The current device's status words (looked up once per device).
 int* status_ptr() {
   static std::atomic<int*> cache[64];
   int dev = 0;
@@ -245,10 +246,12 @@ int fa_debug_set_timing_events(void* before_main, void* after_main) {
 
 int fa_last_device_status(void* stream) {
   if (cudaStreamSynchronize(static_cast<cudaStream_t>(stream)) != cudaSuccess) return FA_ERR_CUDA;
-  int v = 0, zero = 0;
-  if (cudaMemcpyFromSymbol(&v, g_device_status, sizeof(int)) != cudaSuccess) return FA_ERR_CUDA;
-  if (v != 0 && cudaMemcpyToSymbol(g_device_status, &zero, sizeof(int)) != cudaSuccess) return FA_ERR_CUDA;
-  return v;
+  int v[2] = {0, 0}, zero = 0;
+  if (cudaMemcpyFromSymbol(v, g_device_status, sizeof(v)) != cudaSuccess) return FA_ERR_CUDA;
+  const int which = v[0] != 0 ? 0 : 1;   // the other one is left for the next call
+  if (v[which] != 0 && cudaMemcpyToSymbol(g_device_status, &zero, sizeof(int), which * sizeof(int)) != cudaSuccess)
+    return FA_ERR_CUDA;
+  return v[which];
 }
 
 static int fwd_impl(const void* q, const void* k, const void* v, void* o, float* lse, int B, int H, int Hkv,

@@ -162,7 +162,7 @@ struct Kv4Cache {
   int page_shift;      // page = 1 << page_shift tokens
   int max_pages;
   int Hkv;
-  int* status;         // device status word
+  int* status;         // device status words: of waits, of pages
 };
 
 struct Kv4Join;

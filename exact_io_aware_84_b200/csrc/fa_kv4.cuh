@@ -49,6 +49,8 @@ __device__ __forceinline__ int kv4_count(const Kv4Cache& c, int b, int T) {
   return n < 0 ? 0 : (n > T ? T : n);
 }
 
+__device__ __forceinline__ void kv4_no_page(const Kv4Cache& c) { atomicCAS(c.status + 1, 0, FA_ERR_PAGE); }
+
 // Byte address of the block that holds position pos of sequence b, head h, or
 // null (and FA_ERR_PAGE recorded) where no such block exists.
 __device__ __forceinline__ uint8_t* kv4_block_of(const Kv4Cache& c, int b, int h, long long pos, int block_bytes) {
@@ -60,7 +62,7 @@ __device__ __forceinline__ uint8_t* kv4_block_of(const Kv4Cache& c, int b, int h
       return c.pool + (((size_t)pg * c.Hkv + h) * per_page + sub) * (size_t)block_bytes;
     }
   }
-  atomicCAS(c.status, 0, FA_ERR_PAGE);
+  kv4_no_page(c);
   return nullptr;
 }
 

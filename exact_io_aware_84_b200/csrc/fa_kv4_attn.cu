@@ -311,7 +311,7 @@ __global__ void __launch_bounds__(kThreads, (Shape<D, NT, C>::CtasPerSm)) fa_kv4
     if (x.b < p.B - 1) r = reach(++x.b);
   };
   auto past_table = [&](const Reach& r) {
-    if (r.n > 0 && r.start + r.n > r.keys && r.start + r.n > 0) atomicCAS(p.c.status, 0, FA_ERR_PAGE);
+    if (r.n > 0 && r.start + r.n > r.keys && r.start + r.n > 0) kv4_no_page(p.c);
   };
 
   // ---- which steps are this warp's
@@ -421,7 +421,7 @@ __global__ void __launch_bounds__(kThreads, (Shape<D, NT, C>::CtasPerSm)) fa_kv4
   auto produce = [&](int make, int ahead, int to) {
     if (make == 0) {
       const bool ok = page_next >= 0 && page_next < p.c.n_pages;
-      if (!ok && page_next != -2) atomicCAS(p.c.status, 0, FA_ERR_PAGE);
+      if (!ok && page_next != -2) kv4_no_page(p.c);
       bytes = ok ? Block : 0;
       src = p.c.pool + (((size_t)(ok ? page_next : 0) * p.c.Hkv << per_page_shift) + in_page_next) * (size_t)Block;
       have = __ballot_sync(0xffffffffu, ok);

@@ -354,9 +354,10 @@ const char* fa_status_string(int status);
 
 /*
  * Synchronises `stream`, then returns FA_ERR_TIMEOUT if any kernel of this
- * library on the current device gave up on a pipeline wait since the last
- * call, FA_ERR_PAGE if one met a cache position without a page (the first of
- * the two to happen; FA_OK if neither), and clears that record.  Returns
+ * library on the current device gave up on a pipeline wait since that was last
+ * reported, else FA_ERR_PAGE if one met a cache position without a page since
+ * that was, else FA_OK; and clears the record that it returns.  After both the
+ * first call returns FA_ERR_TIMEOUT and the second FA_ERR_PAGE.  Returns
  * FA_ERR_CUDA if the synchronisation itself fails.
  */
 int fa_last_device_status(void* stream);

@@ -264,3 +264,34 @@ def test_an_idle_sequence_s_pages_are_not_looked_at(idle, d):
     _ok()
     used = (c.pool != before).flatten(1).any(1).nonzero().flatten().tolist()
     assert used in ([], [int(c.table[0, 0])])
+
+
+# ---------------------------------------------------------------- statuses
+
+
+@pytest.mark.parametrize("page_first", [True, False])
+def test_a_missing_page_does_not_hide_a_timeout(page_first):
+    c = Cache(1, 2, 128, "bf16", 16, 200, seed=41)
+    c.write([0], 200)
+    q = _rows(c.g, "bf16", 1, 8, 1, 128).cuda()
+    k = _rows(c.g, "bf16", 1, 2, 1, 128).cuda()
+    _ok()
+
+    def no_page():
+        fa.fa_kv4_write(k, k, c.pool, c.table, _ints([c.per * 16]))
+
+    if page_first:
+        no_page()
+    assert fa.fa_debug_set_wait_limit_ms(100) == fa.FA_OK
+    assert fa.fa_debug_set_flags(4) == fa.FA_OK
+    try:
+        fa.fa_fwd_kv4(q, c.pool, c.table, _ints([199]))
+        torch.cuda.synchronize()
+    finally:
+        fa.fa_debug_set_flags(0)
+        fa.fa_debug_set_wait_limit_ms(1000)
+    if not page_first:
+        no_page()
+    assert fa.fa_last_device_status() == fa.FA_ERR_TIMEOUT
+    assert fa.fa_last_device_status() == fa.FA_ERR_PAGE
+    _ok()
