@@ -295,3 +295,21 @@ def test_a_missing_page_does_not_hide_a_timeout(page_first):
     assert fa.fa_last_device_status() == fa.FA_ERR_TIMEOUT
     assert fa.fa_last_device_status() == fa.FA_ERR_PAGE
     _ok()
+
+
+# ---------------------------------------------------------------- queries and scales at the ends
+
+
+@pytest.mark.parametrize("wide", [False, True])
+@pytest.mark.parametrize("dtype", ["bf16", "fp16"])
+@pytest.mark.parametrize("scale", [1e-20, 1e-25, 1e-38, 1e-45])
+def test_rows_of_zeros_under_a_tiny_scale(scale, dtype, wide):
+    """Every key that a row sees has the same weight, and those that it does not see have none."""
+    c = Cache(2, 1, 64, dtype, 16, 150, seed=42)
+    c.write([0, 0], 150)
+    if wide:
+        _room(c)
+    q = torch.zeros(2, 4, 3, 64, dtype=TYPES[dtype])
+    q[:, 1] = _rows(c.g, dtype, 2, 3, 64)
+    attend(c, q, [100, 3], scale=scale)
+    _ok()
