@@ -195,26 +195,41 @@ __device__ __forceinline__ float* slot_of(const Kv4FwdParams& p, long long worke
   return p.partials + (size_t)(2 * worker + which) * slot_floats;
 }
 
-// Part of a row's result: O weighted by l, the maximum m (in log2) and sum l.
+// Part of a row's result: O, the maximum m (in log2) and sum l.  l = 0: no key.
 struct Piece {
   float4 o;
   float m, l;
 
-  // The two as one; o stays a sum weighted by l.
-  __device__ __forceinline__ void add(const float4& x, float xm, float xl) {
-    const float top = fmaxf(m, xm);
-    const float fa = ex2_approx(m - top), fb = ex2_approx(xm - top);
-    o.x = o.x * fa + x.x * fb, o.y = o.y * fa + x.y * fb;
-    o.z = o.z * fa + x.z * fb, o.w = o.w * fa + x.w * fb;
-    l = l * fa + xl * fb;
+  // With N more, each O[i] with its m and l.  O stays an average, under weights
+  // of at most 1: no sum overflows that O itself does not.
+  template <int N>
+  __device__ __forceinline__ void add(const float4 (&x)[N], const float2 (&ml)[N]) {
+    float top = m;
+#pragma unroll
+    for (int i = 0; i < N; ++i) top = fmaxf(top, ml[i].x);
+    float sum = l * ex2_approx(m - top), w[N];
+    const float mine = sum;
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+      w[i] = ml[i].y * ex2_approx(ml[i].x - top);
+      sum += w[i];
+    }
+    const float inv = sum > 0.f ? __fdividef(1.f, sum) : 0.f;
+    const float keep = mine * inv;
+    o.x *= keep, o.y *= keep, o.z *= keep, o.w *= keep;
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+      const float y = w[i] * inv;
+      o.x += x[i].x * y, o.y += x[i].y * y, o.z += x[i].z * y, o.w += x[i].w * y;
+    }
     m = top;
+    l = sum;
   }
 };
 
 template <bool BF16>
 __device__ __forceinline__ void store_result(const Kv4FwdParams& p, const Piece& x, long long row, int D, int col) {
-  const float inv = x.l == 0.f ? 0.f : 1.f / x.l;
-  const float4 o = make_float4(x.o.x * inv, x.o.y * inv, x.o.z * inv, x.o.w * inv);
+  const float4 o = x.o;
   if (p.o32)
     *reinterpret_cast<float4*>(static_cast<float*>(p.o) + row * D + col) = o;
   else
@@ -248,17 +263,19 @@ __device__ __forceinline__ void join_in_cluster(const Kv4FwdParams& p, const uin
     for (int r = 0; r < p.cluster; ++r) {
       uint32_t there;
       asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(there) : "r"(base), "r"(r));
+      float4 x[kWarps];
+      float2 ml[kWarps];
 #pragma unroll
       for (int w = 0; w < kWarps; ++w) {
         const uint32_t at = there + w * Sh::Stages * Sh::Stage;
-        float4 x;
-        float m, l;
         asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
-                     : "=f"(x.x), "=f"(x.y), "=f"(x.z), "=f"(x.w)
+                     : "=f"(x[w].x), "=f"(x[w].y), "=f"(x[w].z), "=f"(x[w].w)
                      : "r"(at + (row * D + col) * 4));
-        asm volatile("ld.shared::cluster.v2.f32 {%0, %1}, [%2];" : "=f"(m), "=f"(l) : "r"(at + (Sh::Rows * D + 2 * row) * 4));
-        sum.add(make_float4(x.x * l, x.y * l, x.z * l, x.w * l), m, l);
+        asm volatile("ld.shared::cluster.v2.f32 {%0, %1}, [%2];"
+                     : "=f"(ml[w].x), "=f"(ml[w].y)
+                     : "r"(at + (Sh::Rows * D + 2 * row) * 4));
       }
+      sum.add(x, ml);
     }
     store_result<BF16>(p, sum, row0 + row, D, col);
   }
@@ -900,19 +917,17 @@ __global__ void __launch_bounds__(kJoinThreads) fa_kv4_join_kernel(const Kv4FwdP
           x[i] = *reinterpret_cast<const float4*>(part + row * D + col);
         }
       }
-#pragma unroll
-      for (int i = 0; i < kFly; ++i) {
-        const float l = ml[i].y;
-        sum.add(make_float4(x[i].x * l, x[i].y * l, x[i].z * l, x[i].w * l), ml[i].x, l);
-      }
+      sum.add(x, ml);
     }
     shared[threadIdx.x] = sum;
   }
   __syncthreads();
   if (turn != 0) return;
   for (int k = 1; k < turns; ++k) {
-    const Piece x = shared[k * items + item];
-    sum.add(x.o, x.m, x.l);
+    const Piece& other = shared[k * items + item];
+    const float4 x[1] = {other.o};
+    const float2 ml[1] = {make_float2(other.m, other.l)};
+    sum.add(x, ml);
   }
   store_result<BF16>(p, sum, j.row + row, D, col);
 }

@@ -313,3 +313,26 @@ def test_rows_of_zeros_under_a_tiny_scale(scale, dtype, wide):
     q[:, 1] = _rows(c.g, dtype, 2, 3, 64)
     attend(c, q, [100, 3], scale=scale)
     _ok()
+
+
+@pytest.mark.parametrize("wide", [False, True])
+@pytest.mark.parametrize("o_fp32", [True, False])
+@pytest.mark.parametrize("H,d", [(1, 64), (4, 128), (8, 128), (12, 64)])
+def test_values_at_the_end_of_bf16_s_range(H, d, o_fp32, wide):
+    """Infinities are held as the largest finite values, and O, an average of them, is finite."""
+    inf = float("inf")
+    c = Cache(1, 1, d, "bf16", 16, 1500, seed=43)
+    k = _rows(c.g, "bf16", 1, 1, 1500, d)
+    k[:, :, 700:] *= 2
+    c.write([0], 1500, k=k, v=torch.full((1, 1, 1500, d), inf, dtype=torch.bfloat16))
+    if wide:
+        _room(c)
+    q = _rows(c.g, "bf16", 1, H, 1, d)
+    for at in (0, 40, 1499):
+        attend(c, q, [at], o_fp32=o_fp32)
+    v = _rows(c.g, "bf16", 1, 1, 1500, d)
+    v[:, :, 3::7, :40], v[:, :, 5::11, 40:] = inf, -inf
+    c.write([0], 1500, v=v)
+    for at in (40, 1499):
+        attend(c, q, [at], o_fp32=o_fp32)
+    _ok()
