@@ -191,6 +191,17 @@ struct Reach {
   }
 };
 
+// Two elements of O in 16 bits.  O is an average of finite values, but P s_V's
+// rounding can put it half a step past fp16's largest (bf16's is further off).
+template <bool BF16>
+__device__ __forceinline__ uint32_t pack_o(float a, float b) {
+  if constexpr (!BF16) {
+    a = fabsf(a) > 65504.f ? copysignf(65504.f, a) : a;
+    b = fabsf(b) > 65504.f ? copysignf(65504.f, b) : b;
+  }
+  return pack2<BF16>(a, b);
+}
+
 __device__ __forceinline__ float* slot_of(const Kv4FwdParams& p, long long worker, int which, int slot_floats) {
   return p.partials + (size_t)(2 * worker + which) * slot_floats;
 }
@@ -234,7 +245,7 @@ __device__ __forceinline__ void store_result(const Kv4FwdParams& p, const Piece&
     *reinterpret_cast<float4*>(static_cast<float*>(p.o) + row * D + col) = o;
   else
     *reinterpret_cast<uint2*>(static_cast<uint16_t*>(p.o) + row * D + col) =
-        make_uint2(pack2<BF16>(o.x, o.y), pack2<BF16>(o.z, o.w));
+        make_uint2(pack_o<BF16>(o.x, o.y), pack_o<BF16>(o.z, o.w));
   if (col == 0) p.lse[row] = (x.m + log2f(x.l)) * 0.69314718055994531f;
 }
 
@@ -836,7 +847,7 @@ __global__ void __launch_bounds__(kThreads, (Shape<D, NT, C>::CtasPerSm)) fa_kv4
             *reinterpret_cast<float4*>(static_cast<float*>(p.o) + (row0 + row) * D + col) = x;
           else
             *reinterpret_cast<uint2*>(static_cast<uint16_t*>(p.o) + (row0 + row) * D + col) =
-                make_uint2(pack2<BF16>(x.x, x.y), pack2<BF16>(x.z, x.w));
+                make_uint2(pack_o<BF16>(x.x, x.y), pack_o<BF16>(x.z, x.w));
         }
         if (g == 0 && column_class == 0) {
           if (part != nullptr)

@@ -336,3 +336,38 @@ def test_values_at_the_end_of_bf16_s_range(H, d, o_fp32, wide):
     for at in (40, 1499):
         attend(c, q, [at], o_fp32=o_fp32)
     _ok()
+
+
+@pytest.mark.parametrize("wide", [False, True])
+@pytest.mark.parametrize("o_fp32", [True, False])
+@pytest.mark.parametrize("H,T,d", [(1, 1, 64), (4, 1, 128), (8, 1, 128), (12, 1, 64), (40, 10, 128)])
+def test_values_at_the_end_of_fp16_s_range(H, T, d, o_fp32, wide):
+    inf = float("inf")
+    c = Cache(1, 1, d, "fp16", 16, 1500, seed=44)
+    v = torch.full((1, 1, 1500, d), inf, dtype=torch.float16)
+    v[..., 1::2] = -inf
+    c.write([0], 1500, v=v)
+    if wide:
+        _room(c)
+    q = _rows(c.g, "fp16", 1, H, T, d)
+    for at in (0, 3, 40, 1499 - T):
+        o, _ = attend(c, q, [at], o_fp32=o_fp32)
+        assert torch.isfinite(o).all()
+    _ok()
+
+
+@pytest.mark.parametrize("T", [1, 12])
+def test_one_key_s_rounding_does_not_take_fp16_past_its_range(T):
+    """A key below the running maximum's move has nearly all the weight, which rounds: up by more than 2^-12 in some
+    rows.  Every O is 65504; P s_V and the weights round by 2^-11, O's sums by 2^-13, O itself by 2^-11."""
+    B, d, page = 600, 128, 64
+    g = torch.Generator().manual_seed(45)
+    pool = fa.fa_kv4_pool(B * 4, 2, page, d)
+    table = torch.randperm(B * 4, generator=g).reshape(B, 4).to(torch.int32).cuda()
+    k = torch.full((B, 2, 256, d), -2.0, dtype=torch.float16, device="cuda")
+    k[:, :, 0], k[:, :, 80] = 0.0, 0.35
+    fa.fa_kv4_write(k, torch.full_like(k, float("inf")), pool, table, _ints([0] * B))
+    q = (_rows(g, "fp16", B, 2, T, d).float() * 0.2 + 0.5).half()
+    o, _ = fa.fa_fwd_kv4(q.cuda(), pool, table, _ints([255 - T] * B), causal=True)
+    assert ((o.float() - 65504).abs() <= 65504 * (2.0**-10 + 2.0**-13)).all()
+    _ok()
