@@ -12,7 +12,9 @@ sm_100 device is present, the calls raise.
 from __future__ import annotations
 
 import ctypes
+import importlib.util
 import os
+import warnings
 from typing import Optional
 
 __all__ = [
@@ -552,26 +554,43 @@ def _check_kv4(pool, page_table, start, count, like, B, Hkv, d):
     return n_pages, 16 * blocks, table_shape[1]
 
 
-_SERVE = None
+_SERVE = None   # the compiled binding; False where there is none
+
+
+def _serve_path() -> str:
+    return os.path.join(os.path.dirname(os.path.abspath(__file__)), "_serve.so")
+
+
+def _load_serve():
+    """The compiled binding, connected to the library; False where it has not
+    been built or does not load, for the serving calls do without it."""
+    path = _serve_path()
+    if not os.path.exists(path):
+        return False
+    name = __name__ + "._serve"
+    spec = importlib.util.spec_from_file_location(name, path)
+    try:
+        module = importlib.util.module_from_spec(spec)
+        spec.loader.exec_module(module)
+    except ImportError as e:
+        warnings.warn(f"the serving calls' compiled binding does not load ({e}): they go through ctypes", RuntimeWarning)
+        return False
+    lib = load_library()
+    module.connect(*(ctypes.cast(getattr(lib, fn), _vp).value
+                     for fn in ("fa_kv4_write", "fa_kv4_read", "fa_fwd_kv4", "fa_fwd_kv4_workspace_size")))
+    return module
 
 
 def _compiled(t):
     """The compiled binding of the serving calls, or None for what is not a
-    CUDA tensor or where it has not been built.  Its functions return None for
+    CUDA tensor or where there is none.  Its functions return None for
     arguments that they do not take."""
     global _SERVE
     if _SERVE is None:
         if type(t) is not _torch().Tensor or not t.is_cuda:
             return None
-        path = os.path.join(os.path.dirname(os.path.abspath(__file__)), "_serve.so")
-        if not os.path.exists(path):
-            return None
-        lib = load_library()
-        from . import _serve as module
-        module.connect(*(ctypes.cast(getattr(lib, name), _vp).value
-                         for name in ("fa_kv4_write", "fa_kv4_read", "fa_fwd_kv4", "fa_fwd_kv4_workspace_size")))
-        _SERVE = module
-    return _SERVE
+        _SERVE = _load_serve()
+    return _SERVE or None
 
 
 def _allocating_on(stream, device, allocate):
