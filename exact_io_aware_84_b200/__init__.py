@@ -558,7 +558,11 @@ _SERVE = None   # the compiled binding; False where there is none
 
 
 def _serve_path() -> str:
-    return os.path.join(os.path.dirname(os.path.abspath(__file__)), "_serve.so")
+    """Where the compiled binding lies for this Python and this torch, whose
+    headers it is compiled against: one of others is not looked at."""
+    import sysconfig
+    tag = f"{sysconfig.get_config_var('SOABI')}-torch{_torch().__version__}"
+    return os.path.join(os.path.dirname(os.path.abspath(__file__)), f"_serve.{tag}.so")
 
 
 def _load_serve():

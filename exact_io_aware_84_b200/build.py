@@ -4,7 +4,8 @@ Usage: ``python -m exact_io_aware_84_b200.build [-v]``.  Each ``csrc/*.cu``
 is compiled to an object in ``_build/`` (in parallel), then linked into
 ``exact_io_aware_84_b200/libfa.so``.  Objects are rebuilt when their source
 or any header changed.  ``csrc/fa_serve.cpp``, the serving calls' binding to
-torch tensors, becomes the module ``exact_io_aware_84_b200/_serve.so``.
+torch tensors, becomes the module ``exact_io_aware_84_b200/_serve.*.so``, whose
+name holds the versions of Python and torch that it was compiled for.
 """
 
 from __future__ import annotations
@@ -22,7 +23,6 @@ CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 BUILD = os.path.join(ROOT, "_build")
 LIB = os.path.join(PKG, "libfa.so")
-SERVE = os.path.join(PKG, "_serve.so")
 
 ARCH = ["-gencode", "arch=compute_100a,code=sm_100a"]
 NVCC_FLAGS = ["-O3", "-std=c++17", "-lineinfo", "-Xcompiler", "-fPIC", "--expt-relaxed-constexpr",
@@ -52,27 +52,30 @@ def _compile(src: str, obj: str, verbose: bool, ptxas_v: bool) -> str:
     return (r.stdout + r.stderr) if (verbose or ptxas_v) else ""
 
 
-def _build_serve() -> None:
-    """_serve.so against the running interpreter's Python and torch headers."""
+def _build_serve(force: bool = False) -> None:
+    """_serve.*.so against the running interpreter's Python and torch headers,
+    whose versions are in its name."""
     import sysconfig
 
     import torch
 
-    src = os.path.join(CSRC, "fa_serve.cpp")
-    if os.path.exists(SERVE) and os.path.getmtime(SERVE) >= max(os.path.getmtime(src), _headers_mtime()):
+    from . import _serve_path
+
+    src, so = os.path.join(CSRC, "fa_serve.cpp"), _serve_path()
+    if not force and os.path.exists(so) and os.path.getmtime(so) >= max(os.path.getmtime(src), _headers_mtime()):
         return
     home = os.path.dirname(torch.__file__)
     cuda = os.path.dirname(os.path.dirname(os.path.realpath(nvcc_path())))
     dirs = [INCLUDE, sysconfig.get_paths()["include"], os.path.join(home, "include"),
             os.path.join(home, "include", "torch", "csrc", "api", "include"), os.path.join(cuda, "include")]
-    tmp = SERVE + ".tmp"
+    tmp = f"{so}.{os.getpid()}.tmp"
     cmd = ["g++", "-O2", "-std=c++17", "-fPIC", "-shared", f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
            *(f"-I{d}" for d in dirs), src, "-o", tmp, "-L" + os.path.join(home, "lib"), "-lc10", "-ltorch_cpu",
            "-ltorch_python", "-lc10_cuda"]
     r = subprocess.run(cmd, capture_output=True, text=True)
     if r.returncode != 0:
         raise RuntimeError(f"g++ failed for fa_serve.cpp:\n{r.stdout}\n{r.stderr}")
-    os.replace(tmp, SERVE)
+    os.replace(tmp, so)
 
 
 def build(verbose: bool = False, force: bool = False, ptxas_v: bool = False) -> str:
@@ -98,7 +101,7 @@ def build(verbose: bool = False, force: bool = False, ptxas_v: bool = False) -> 
         if r.returncode != 0:
             raise RuntimeError(f"link failed:\n{r.stdout}\n{r.stderr}")
         os.replace(tmp, LIB)
-    _build_serve()
+    _build_serve(force)
     return LIB
 
 

@@ -4,10 +4,13 @@ import os
 import shutil
 import subprocess
 
+import sysconfig
+
 import pytest
 import torch
 
 import exact_io_aware_84_b200 as fa
+from exact_io_aware_84_b200 import build
 
 HAVE_CC = shutil.which("gcc") is not None
 
@@ -23,7 +26,7 @@ def fresh(monkeypatch):
     """_compiled as in a process that has not called it yet, for a tensor that passes for a CUDA one."""
     monkeypatch.setattr(fa, "_SERVE", None)
     t = torch.empty(0).as_subclass(_CudaTensor)
-    monkeypatch.setattr(fa, "_torch", lambda: type("torch", (), {"Tensor": _CudaTensor}))
+    monkeypatch.setattr(fa, "_torch", lambda: type("torch", (), {"Tensor": _CudaTensor, "__version__": torch.__version__}))
     return t
 
 
@@ -50,7 +53,55 @@ def test_no_binding_leaves_the_other_way(fresh, monkeypatch, tmp_path):
 
 def test_the_binding_that_is_built_loads(fresh):
     if not os.path.exists(fa._serve_path()):
-        pytest.skip("_serve.so not built")
+        pytest.skip("the binding is not built")
     module = fa._compiled(fresh)
     assert module is not None and module is fa._compiled(fresh)
     assert all(callable(getattr(module, name)) for name in ("write", "read", "fwd"))
+
+
+def test_a_binding_of_another_python_or_torch_is_not_looked_at(monkeypatch):
+    here = fa._serve_path()
+    monkeypatch.setattr(torch, "__version__", "1.2.3")
+    other = fa._serve_path()
+    monkeypatch.setattr(sysconfig, "get_config_var", lambda name: "cpython-299-x86_64-linux-gnu")
+    assert len({here, other, fa._serve_path()}) == 3
+
+
+@pytest.fixture
+def compiler(monkeypatch, tmp_path):
+    """Commands that the build of the binding runs, none of which is run; the binding lies in tmp_path."""
+    ran = []
+
+    def run(cmd, **kw):
+        ran.append(cmd)
+        with open(cmd[cmd.index("-o") + 1], "wb") as f:
+            f.write(b"built")
+        return subprocess.CompletedProcess(cmd, 0, "", "")
+
+    monkeypatch.setattr(subprocess, "run", run)
+    monkeypatch.setattr(build, "nvcc_path", lambda: "/usr/local/cuda/bin/nvcc")
+    monkeypatch.setattr(fa, "_serve_path", lambda: str(tmp_path / "_serve.x.so"))
+    return ran
+
+
+def test_the_binding_is_built_when_it_is_old_or_asked_for(compiler, tmp_path):
+    so = tmp_path / "_serve.x.so"
+    build._build_serve()
+    assert so.read_bytes() == b"built" and len(compiler) == 1
+    build._build_serve()
+    assert len(compiler) == 1
+    build._build_serve(force=True)
+    assert len(compiler) == 2
+    os.utime(so, (1, 1))
+    build._build_serve()
+    assert len(compiler) == 3 and [p.name for p in tmp_path.iterdir()] == ["_serve.x.so"]
+
+
+def test_a_forced_build_reaches_the_binding(monkeypatch):
+    asked = []
+    monkeypatch.setattr(build, "_compile", lambda *a: "")
+    monkeypatch.setattr(subprocess, "run", lambda cmd, **kw: subprocess.CompletedProcess(cmd, 0, "", ""))
+    monkeypatch.setattr(os, "replace", lambda a, b: None)
+    monkeypatch.setattr(build, "_build_serve", lambda force=False: asked.append(force))
+    build.build(force=True)
+    assert asked == [True]
