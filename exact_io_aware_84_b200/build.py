@@ -5,7 +5,8 @@ is compiled to an object in ``_build/`` (in parallel), then linked into
 ``exact_io_aware_84_b200/libfa.so``.  Objects are rebuilt when their source
 or any header changed.  ``csrc/fa_serve.cpp``, the serving calls' binding to
 torch tensors, becomes the module ``exact_io_aware_84_b200/_serve.*.so``, whose
-name holds the versions of Python and torch that it was compiled for.
+name holds the versions of Python and torch that it was compiled for; without
+torch, g++ or Python's headers the build goes on without it.
 """
 
 from __future__ import annotations
@@ -16,6 +17,7 @@ import os
 import shutil
 import subprocess
 import sys
+import warnings
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
@@ -57,12 +59,18 @@ def _build_serve(force: bool = False) -> None:
     whose versions are in its name."""
     import sysconfig
 
+    src = os.path.join(CSRC, "fa_serve.cpp")
+    newest = max(os.path.getmtime(src), _headers_mtime())
+    for old in glob.glob(os.path.join(PKG, "_serve*.so")):   # of any version: none outlives its sources
+        if os.path.getmtime(old) < newest:
+            os.remove(old)
+
     import torch
 
     from . import _serve_path
 
-    src, so = os.path.join(CSRC, "fa_serve.cpp"), _serve_path()
-    if not force and os.path.exists(so) and os.path.getmtime(so) >= max(os.path.getmtime(src), _headers_mtime()):
+    so = _serve_path()
+    if os.path.exists(so) and not force:
         return
     home = os.path.dirname(torch.__file__)
     cuda = os.path.dirname(os.path.dirname(os.path.realpath(nvcc_path())))
@@ -101,7 +109,10 @@ def build(verbose: bool = False, force: bool = False, ptxas_v: bool = False) -> 
         if r.returncode != 0:
             raise RuntimeError(f"link failed:\n{r.stdout}\n{r.stderr}")
         os.replace(tmp, LIB)
-    _build_serve(force)
+    try:
+        _build_serve(force)
+    except (ImportError, OSError, RuntimeError) as e:   # no torch, no compiler, no headers
+        warnings.warn(f"the serving calls' compiled binding was not built, they go through ctypes: {e}", RuntimeWarning)
     return LIB
 
 

@@ -3,7 +3,7 @@
 import os
 import shutil
 import subprocess
-
+import sys
 import sysconfig
 
 import pytest
@@ -80,6 +80,7 @@ def compiler(monkeypatch, tmp_path):
 
     monkeypatch.setattr(subprocess, "run", run)
     monkeypatch.setattr(build, "nvcc_path", lambda: "/usr/local/cuda/bin/nvcc")
+    monkeypatch.setattr(build, "PKG", str(tmp_path))
     monkeypatch.setattr(fa, "_serve_path", lambda: str(tmp_path / "_serve.x.so"))
     return ran
 
@@ -105,3 +106,30 @@ def test_a_forced_build_reaches_the_binding(monkeypatch):
     monkeypatch.setattr(build, "_build_serve", lambda force=False: asked.append(force))
     build.build(force=True)
     assert asked == [True]
+
+
+@pytest.mark.parametrize("missing", ["torch", "compiler", "headers"])
+def test_the_library_is_built_where_the_binding_cannot_be(missing, compiler, monkeypatch, tmp_path):
+    """What is there of older bindings goes, as the library that they were built for does."""
+    monkeypatch.setattr(build, "_compile", lambda *a: "")
+    so = tmp_path / "_serve.x.so"
+    so.write_bytes(b"old")
+    os.utime(so, (1, 1))
+    lib = tmp_path / "libfa.so"
+    monkeypatch.setattr(build, "LIB", str(lib))
+    run = subprocess.run
+
+    def no_binding(cmd, **kw):
+        if cmd[0] != "g++":
+            return run(cmd, **kw)
+        if missing == "compiler":
+            raise FileNotFoundError("g++")
+        return subprocess.CompletedProcess(cmd, 1, "", "Python.h: No such file or directory")
+
+    monkeypatch.setattr(subprocess, "run", no_binding)
+    if missing == "torch":
+        monkeypatch.setitem(sys.modules, "torch", None)
+    with pytest.warns(RuntimeWarning, match="not built"):
+        assert build.build() == str(lib)
+    assert lib.read_bytes() == b"built"
+    assert not so.exists()
