@@ -530,7 +530,8 @@ int fa_convert(void* dst, const float* src, long long n, int dst_dtype, void* st
 size_t fa_kv4_pool_bytes(int n_pages, int Hkv, int page, int d) {
   int shift;
   if (kv4_check_sizes(1, Hkv, Hkv, 1, d, n_pages, page, 1, &shift) != FA_OK) return 0;
-  return (size_t)n_pages * Hkv * (page / kKv4Block) * kv4_block_bytes(d);
+  const size_t heads = (size_t)n_pages * Hkv, each = (size_t)(page / kKv4Block) * kv4_block_bytes(d);
+  return heads <= SIZE_MAX / 2 / each ? heads * each : 0;
 }
 
 // fa_kv4_write and fa_kv4_read: the same arguments, k and v in or out.

@@ -305,7 +305,8 @@ int fa_fwd_fp8(const void* q, const void* k, const void* v, void* o, float* lse,
  * [0, n_pages), does not exist: it is not written, reads as zeros, is left out
  * as a key, and fa_last_device_status() reports FA_ERR_PAGE.
  *
- * fa_kv4_pool_bytes: bytes of a pool, or 0 for invalid sizes.
+ * fa_kv4_pool_bytes: bytes of a pool, or 0 for invalid sizes (those of a pool
+ *   of 2^63 bytes or more among them).
  *
  * fa_kv4_write: k, v [B, Hkv, T, d], dtype (FA_BF16 or FA_FP16), are quantised
  *   into the cache.  Bytes of other tokens are left as they are.  Two tokens at

@@ -133,3 +133,16 @@ def test_the_library_is_built_where_the_binding_cannot_be(missing, compiler, mon
         assert build.build() == str(lib)
     assert lib.read_bytes() == b"built"
     assert not so.exists()
+
+
+# ---------------------------------------------------------------- sizes at the ends
+
+
+def test_no_pool_has_more_bytes_than_an_address_reaches():
+    most = (1 << 31) - 1
+    assert fa.fa_kv4_pool_bytes(most, 1, 16, 64) == most * 18 * 64
+    assert fa.fa_kv4_pool_bytes(most, 1 << 16, 256, 128) == most * (1 << 16) * 16 * 18 * 128      # below 2^63
+    for heads in (1 << 17, 1 << 18, 1 << 22, most):
+        assert fa.fa_kv4_pool_bytes(most, heads, 256, 128) == 0
+    with pytest.raises(ValueError):
+        fa.fa_kv4_pool(most, 1 << 22, 256, 128, device="cpu")
