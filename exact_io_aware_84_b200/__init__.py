@@ -513,8 +513,15 @@ def _dense_cuda(name, t, dtypes, ref=None):
         raise ValueError(f"{name} must be on the same device as the other arguments")
 
 
+def _sizes(*sizes):
+    """The sizes as the library takes them, or None where one does not fit: ctypes would cut it to 32 bits."""
+    sizes = [int(x) for x in sizes]
+    return sizes if all(-(1 << 31) <= x < 1 << 31 for x in sizes) else None
+
+
 def fa_kv4_pool_bytes(n_pages: int, Hkv: int, page: int, d: int) -> int:
-    return int(load_library().fa_kv4_pool_bytes(int(n_pages), int(Hkv), int(page), int(d)))
+    sizes = _sizes(n_pages, Hkv, page, d)
+    return 0 if sizes is None else int(load_library().fa_kv4_pool_bytes(*sizes))
 
 
 def fa_kv4_pool(n_pages: int, Hkv: int, page: int, d: int, device="cuda"):
@@ -539,6 +546,8 @@ def _check_kv4(pool, page_table, start, count, like, B, Hkv, d):
     table_shape = page_table.shape
     if len(table_shape) != 2 or table_shape[0] != B:
         raise ValueError(f"page_table must be [B, max_pages] with B = {B}")
+    if _sizes(n_pages, 16 * blocks, table_shape[1]) is None:
+        raise ValueError("n_pages, the page size and max_pages must be below 2^31")
     int32 = torch.int32
     for name, t in (("page_table", page_table), ("start", start), ("count", count)):
         if t is None and name == "count":
@@ -685,7 +694,8 @@ def fa_kv4_read(pool, page_table, start, count=None, N: Optional[int] = None, k=
 
 
 def fa_fwd_kv4_workspace_size(B: int, H: int, Hkv: int, T: int, d: int) -> int:
-    return int(load_library().fa_fwd_kv4_workspace_size(int(B), int(H), int(Hkv), int(T), int(d)))
+    sizes = _sizes(B, H, Hkv, T, d)
+    return 0 if sizes is None else int(load_library().fa_fwd_kv4_workspace_size(*sizes))
 
 
 def fa_fwd_kv4(q, pool, page_table, start, count=None, o=None, lse=None, workspace=None,

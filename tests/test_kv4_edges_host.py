@@ -11,6 +11,7 @@ import torch
 
 import exact_io_aware_84_b200 as fa
 from exact_io_aware_84_b200 import build
+from test_binding_host import _FakeCuda
 
 HAVE_CC = shutil.which("gcc") is not None
 
@@ -146,3 +147,23 @@ def test_no_pool_has_more_bytes_than_an_address_reaches():
         assert fa.fa_kv4_pool_bytes(most, heads, 256, 128) == 0
     with pytest.raises(ValueError):
         fa.fa_kv4_pool(most, 1 << 22, 256, 128, device="cpu")
+
+
+def test_sizes_past_32_bits_are_not_cut():
+    assert fa.fa_kv4_pool_bytes((1 << 32) + 1, 1, 16, 64) == 0
+    assert fa.fa_kv4_pool_bytes(1, 1 << 32 | 1, 16, 64) == 0
+    assert fa.fa_fwd_kv4_workspace_size((1 << 32) + 2, 8, 2, 1, 128) == 0
+    assert fa.fa_fwd_kv4_workspace_size(2, 8, 2, (1 << 32) + 1, 128) == 0
+    with pytest.raises(ValueError):
+        fa.fa_kv4_pool((1 << 32) + 1, 1, 16, 64, device="cpu")
+
+
+def test_a_table_past_32_bits_is_refused(monkeypatch):
+    monkeypatch.setattr(fa, "load_library", lambda: pytest.fail("the library must not be reached"))
+    rows = _FakeCuda((3, 4, 5, 64))
+    cache = (_FakeCuda((7, 4, 2, 18 * 64), dtype=torch.uint8), _FakeCuda((3, (1 << 32) + 6), dtype=torch.int32),
+             _FakeCuda((3,), dtype=torch.int32))
+    for call in (lambda: fa.fa_kv4_write(rows, rows, *cache), lambda: fa.fa_fwd_kv4(rows, *cache),
+                 lambda: fa.fa_kv4_read(*cache, k=rows, v=rows)):
+        with pytest.raises(ValueError, match="2.31"):
+            call()
