@@ -792,12 +792,13 @@ def _code_only(text):
 
 def kernel_sources_hash():
     """sha1 prefix of the CUDA sources' code (file names and contents without
-    comments, sorted)."""
+    comments, sorted), but for the 4-bit cache's own files: the workloads here
+    run nothing of them."""
     import glob
     import hashlib
     h = hashlib.sha1()
     for f in sorted(glob.glob(os.path.join(ROOT, "exact_io_aware_84_b200", "csrc", "*"))):
-        if f.endswith((".cu", ".cuh", ".h")):
+        if f.endswith((".cu", ".cuh", ".h")) and not os.path.basename(f).startswith("fa_kv4"):
             h.update(os.path.basename(f).encode())
             with open(f, encoding="utf-8") as fh:
                 h.update(_code_only(fh.read()).encode())

@@ -32,27 +32,6 @@ inline cudaError_t launch_chained(void (*kern)(Params...), dim3 grid, dim3 block
   return cudaLaunchKernelEx(&cfg, kern, std::forward<Args>(args)...);
 }
 
-// The same in clusters of `cluster` CTAs.
-template <typename... Params, typename... Args>
-inline cudaError_t launch_chained_clusters(void (*kern)(Params...), dim3 grid, dim3 block, size_t smem,
-                                           cudaStream_t st, int cluster, Args&&... args) {
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = grid;
-  cfg.blockDim = block;
-  cfg.dynamicSmemBytes = smem;
-  cfg.stream = st;
-  cudaLaunchAttribute attr[2];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
-  attr[1].id = cudaLaunchAttributeClusterDimension;
-  attr[1].val.clusterDim.x = (unsigned)cluster;
-  attr[1].val.clusterDim.y = 1;
-  attr[1].val.clusterDim.z = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = 2;
-  return cudaLaunchKernelEx(&cfg, kern, std::forward<Args>(args)...);
-}
-
 constexpr int kBlockM = 128;  // query rows per Q tile (tcgen05 M)
 constexpr int kBlockN = 128;  // keys per K/V tile
 
@@ -151,50 +130,6 @@ cudaError_t launch_merge(int d, int out_kind, float* o, float* lse, const float*
                          void* out, long long rows, int sms, cudaStream_t st);
 cudaError_t launch_accumulate(bool bf16, float* acc, const void* src, long long n, int sms, cudaStream_t st);
 cudaError_t launch_convert(bool bf16, void* dst, const float* src, long long n, int sms, cudaStream_t st);
-
-// 4-bit key/value cache (layout in fa_kv4.cuh): what its calls share.
-struct Kv4Cache {
-  uint8_t* pool;       // [n_pages][Hkv][page/16] blocks
-  const int* table;    // [B][max_pages]
-  const int* start;    // [B]: position of the call's first token
-  const int* count;    // [B] tokens of each sequence, or null (= T)
-  int n_pages;
-  int page_shift;      // page = 1 << page_shift tokens
-  int max_pages;
-  int Hkv;
-  int* status;         // device status words: of waits, of pages
-};
-
-struct Kv4Join;
-
-struct Kv4FwdParams {
-  Kv4Cache c;
-  const void* q;       // [B, H, T, D] 16-bit
-  void* o;             // [B, H, T, D] 16-bit, or fp32 when o32
-  float* lse;          // [B, H, T]
-  int B, H, T;
-  float scale_log2;    // scale * log2(e)
-  int causal;
-  int o32;
-  uint64_t wait_limit_ns;
-  int debug_flags;     // bit 2: withhold one arrival (timeout test)
-  // set by the launch
-  int row_tiles;             // tiles of query rows a key head
-  long long units_per_seq;   // Hkv * row_tiles
-  int cluster;               // CTAs that share a unit, where clusters do
-  int workers;               // warps of the grid, where they do not
-  int join_units;            // joins go by unit, else by worker
-  int join_items;            // fours of elements a CTA of the joining kernel
-  Kv4Join* joins;            // [units or workers]
-  float* partials;           // [workers][2] pieces of results
-};
-
-cudaError_t launch_kv4_write(bool bf16, int d, const Kv4Cache& c, const void* k, const void* v, int B, int T,
-                             cudaStream_t st);
-cudaError_t launch_kv4_read(bool bf16, int d, const Kv4Cache& c, void* k, void* v, int B, int N, cudaStream_t st);
-// Bytes of the attention's workspace; rows = query rows that share a key head.
-size_t kv4_fwd_workspace(int d, long long rows);
-cudaError_t launch_kv4_fwd(bool bf16, int d, const Kv4FwdParams& p, void* workspace, int sms, cudaStream_t st);
 
 int fwd_threads();
 int bwd_threads();
