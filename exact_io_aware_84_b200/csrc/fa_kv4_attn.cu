@@ -521,7 +521,7 @@ __global__ void __launch_bounds__(kThreads, (Shape<D, NT, C>::CtasPerSm)) fa_kv4
       top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
       top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
       int ex = 14 + 127 - (int)(__float_as_uint(top) >> 23);   // top * 2^ex in [2^14, 2^15)
-      ex = ex > 100 ? 100 : ex;
+      ex = ex > 126 ? 126 : ex;                             // for the rest all of bf16 is exact
       // never 0: a masked score is -infinity, and stays that
       const float up = pow2(ex), back = fminf(fmaxf(p.scale_log2 * kUnit * pow2(-ex), 0x1p-149f), 3e38f);
       f[nt][0] = __shfl_sync(0xffffffffu, back, 8 * t);

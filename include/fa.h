@@ -320,15 +320,16 @@ int fa_fwd_fp8(const void* q, const void* k, const void* v, void* o, float* lse,
  *   0 .. start[b] + t when `causal` is set, else 0 .. start[b] + count[b] - 1.
  *   Padding rows and rows that see no key get O = 0, LSE = -inf.  n s enters
  *   unrounded and sums are float32; q is taken relative to its row's largest
- *   element and rounded at 2^-35 of it (elements above 2^-24 of it are exact),
- *   and P s is rounded to fp16 before the product with V's codes: by 2^-11 of
- *   itself down to 2^-20 of the row's largest P s, over the keys that the row
- *   sees, and by 2^-31 of that below.  So a group of 32 of V's elements whose
- *   scales are less than 2^-20 of another group's loses bits (2^-22: 2^-9, ...
- *   2^-31: all).  o, lse, scale as in fa_fwd ([B,H,T,d], [B,H,T]; the *_O_F32
- *   codes store O in float32, as fa_merge takes it).  Any T: what the cache
- *   holds is read once per 8 or 16 rows of the T * H / Hkv that share a key
- *   head, so fa_kv4_read and fa_fwd_gqa suit whole prompts better.
+ *   element and rounded at 2^-35 of it (elements above 2^-24 of it are exact;
+ *   scores hold for scale |q| up to 2^100), and P s is rounded to fp16 before
+ *   the product with V's codes: by 2^-11 of itself down to 2^-20 of the row's
+ *   largest P s, over the keys that the row sees, and by 2^-31 of that below.
+ *   So a group of 32 of V's elements whose scales are less than 2^-20 of
+ *   another group's loses bits (2^-22: 2^-9, ... 2^-31: all).  o, lse, scale as
+ *   in fa_fwd ([B,H,T,d], [B,H,T]; the *_O_F32 codes store O in float32, as
+ *   fa_merge takes it).  Any T: what the cache holds is read once per 8 or 16
+ *   rows of the T * H / Hkv that share a key head.  A prompt's first tokens,
+ *   which see nothing before them, need no cache: fa_fwd_gqa suits them better.
  *   workspace: device buffer of fa_fwd_kv4_workspace_size bytes, 256-byte
  *   aligned, contents ignored on entry; calls that may overlap on the GPU need
  *   one each.

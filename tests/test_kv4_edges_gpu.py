@@ -371,3 +371,17 @@ def test_one_key_s_rounding_does_not_take_fp16_past_its_range(T):
     o, _ = fa.fa_fwd_kv4(q.cuda(), pool, table, _ints([255 - T] * B), causal=True)
     assert ((o.float() - 65504).abs() <= 65504 * (2.0**-10 + 2.0**-13)).all()
     _ok()
+
+
+@pytest.mark.parametrize("wide", [False, True])
+@pytest.mark.parametrize("H,d", [(1, 64), (8, 128), (16, 128)])
+@pytest.mark.parametrize("e", [-124, -116, -90, 60, 100])
+def test_queries_of_any_magnitude_and_keys_that_make_up_for_it(e, H, d, wide):
+    c = Cache(1, 1, d, "bf16", 16, 300, seed=46)
+    k = (torch.randn(1, 1, 300, d, generator=c.g) * 2.0**-e).bfloat16()
+    c.write([0], 300, k=k)
+    if wide:
+        _room(c)
+    q = (torch.randn(1, H, 1, d, generator=c.g) * 2.0**e).bfloat16()
+    attend(c, q, [299], o_fp32=True)
+    _ok()
