@@ -35,14 +35,17 @@
 //     rows belong to one group of 32 elements, as s_V does; with C > 1 they
 //     belong to two, and a row's columns hold P s_V for one group each, so that
 //     C times fewer are made.
-// The running maximum m moves only when a score passes it by 2^8: P stays below
-// 2^8.  v_up follows the row's largest P |s_V| so far in the same way: it falls,
-// bringing that to 2^6 .. 2^7, when a bound on the step's passes 2^15, and it
-// rises as m does, so that what O's sums are relative to does not change with
-// m.  A row thus rounds relative to the products of the keys that it sees: keys
-// of other rows, and keys of no weight whatever their values, have no say.  The
-// bound is the largest P of a lane's keys times the largest |s_V| of any key of
-// theirs; the products themselves are looked at where it passes.  (A factor
+// P is taken relative to 2^m, m 48 below the running maximum where it was last
+// moved (in log2); it moves only when a score passes that maximum by 8.  Weights
+// down to 2^-174 so stay in float32's range, for bf16 values reach 2^128.  v_up
+// follows the row's largest P |s_V| so far in the same way: it falls, bringing
+// that to 2^6 .. 2^7, when a bound on the step's passes 2^15, and it rises as m
+// does, so that what O's sums are relative to does not change with m.  (Where
+// P |s_V| passes 2^120, m rises by 56 instead.)  A row thus rounds relative to
+// the products of the keys that it sees: keys of other rows, and keys of no
+// weight whatever their values, have no say.  The bound is the largest P of a
+// lane's keys times the largest |s_V| of any key of theirs; the products
+// themselves are looked at, as logarithms, where it passes.  (A factor
 // common to a tile's rows and taken from V's scales alone was 2 to 5% faster and
 // lost rows beside a key of large V that they did not see.)  P s_V in fp16 adds
 // 2^-11 a term to an error that O's own rounding to fp16 bounds by 2^-11 (2.1e-4
@@ -85,9 +88,11 @@ constexpr int kThreads = 32 * kWarps;
 constexpr int kSeen = kThreads;         // sequences whose lengths a CTA keeps at hand
 constexpr float kUnit = 16777216.f;     // scores and O are summed in units of 2^-24, the subnormals' step
 constexpr float kLeast = -3.402823466e38f;   // a maximum before the first key
-constexpr float kVPass = 32768.f, kVPassLog2 = 15.f;   // P s_V stays in fp16's range
-constexpr float kMostUp = 0x1p118f;          // P v_up stays finite
-constexpr float kLazy = 8.f;            // log2 by which a score may pass the running maximum
+constexpr float kBelow = 48.f;          // log2 by which m lies below the running maximum when it moves,
+constexpr float kLazy = 56.f;           // and by which a score may pass m
+constexpr float kMostUp = 0x1p70f;      // P v_up stays finite
+constexpr float kVPass = 15.f;          // log2: P |s_V| v_up stays in fp16's range
+constexpr float kMostV = 120.f;         // log2 of a P |s_V| for which v_up would get too small
 
 template <int D, int NT, int C>
 struct Shape {
@@ -179,6 +184,11 @@ __device__ __forceinline__ float lg2_approx(float x) {
 
 __device__ __forceinline__ float pow2(int e) { return __int_as_float((e + 127) << 23); }   // -126 <= e <= 127
 
+// l is about 2^kBelow: as near to 0 as its logarithm gets, for its bits' sake.
+__device__ __forceinline__ float lse_of(float m, float l) {
+  return (m + kBelow + log2f(l * 0x1p-48f)) * 0.69314718055994531f;
+}
+
 // How far a sequence reaches in this call.
 struct Reach {
   int n, keys, steps;   // tokens, keys that the last of them sees, steps of a unit (at least one)
@@ -212,26 +222,30 @@ struct Piece {
   float m, l;
 
   // With N more, each O[i] with its m and l.  O stays an average, under weights
-  // of at most 1: no sum overflows that O itself does not.
+  // of at most 1: no sum overflows that O itself does not.  Where a weight is
+  // small, 2^64 of it goes to O[i], so that it does not underflow.
   template <int N>
   __device__ __forceinline__ void add(const float4 (&x)[N], const float2 (&ml)[N]) {
     float top = m;
 #pragma unroll
     for (int i = 0; i < N; ++i) top = fmaxf(top, ml[i].x);
-    float sum = l * ex2_approx(m - top), w[N];
-    const float mine = sum;
+    float w[N + 1], down[N + 1], sum = 0.f;   // the last one is this piece's
 #pragma unroll
-    for (int i = 0; i < N; ++i) {
-      w[i] = ml[i].y * ex2_approx(ml[i].x - top);
-      sum += w[i];
+    for (int i = 0; i <= N; ++i) {
+      const float at = (i < N ? ml[i].x : m) - top;
+      const bool small = at < -64.f;
+      w[i] = (i < N ? ml[i].y : l) * ex2_approx(small ? at + 64.f : at);
+      down[i] = small ? 0x1p-64f : 1.f;
+      sum = fmaf(w[i], down[i], sum);
     }
     const float inv = sum > 0.f ? __fdividef(1.f, sum) : 0.f;
-    const float keep = mine * inv;
-    o.x *= keep, o.y *= keep, o.z *= keep, o.w *= keep;
+    const float keep = w[N] * inv;
+    o.x = o.x * down[N] * keep, o.y = o.y * down[N] * keep, o.z = o.z * down[N] * keep, o.w = o.w * down[N] * keep;
 #pragma unroll
     for (int i = 0; i < N; ++i) {
       const float y = w[i] * inv;
-      o.x += x[i].x * y, o.y += x[i].y * y, o.z += x[i].z * y, o.w += x[i].w * y;
+      o.x = fmaf(x[i].x * down[i], y, o.x), o.y = fmaf(x[i].y * down[i], y, o.y);
+      o.z = fmaf(x[i].z * down[i], y, o.z), o.w = fmaf(x[i].w * down[i], y, o.w);
     }
     m = top;
     l = sum;
@@ -246,7 +260,7 @@ __device__ __forceinline__ void store_result(const Kv4FwdParams& p, const Piece&
   else
     *reinterpret_cast<uint2*>(static_cast<uint16_t*>(p.o) + row * D + col) =
         make_uint2(pack_o<BF16>(o.x, o.y), pack_o<BF16>(o.z, o.w));
-  if (col == 0) p.lse[row] = (x.m + log2f(x.l)) * 0.69314718055994531f;
+  if (col == 0) p.lse[row] = lse_of(x.m, x.l);
 }
 
 __device__ __forceinline__ void cluster_sync() {
@@ -672,24 +686,25 @@ __global__ void __launch_bounds__(kThreads, (Shape<D, NT, C>::CtasPerSm)) fa_kv4
             top[nt][c] = fmaxf(sc[nt][0][c], sc[nt][0][2 + c]);
 #pragma unroll
             for (int bk = 1; bk < KB; ++bk) top[nt][c] = fmax3(top[nt][c], sc[nt][bk][c], sc[nt][bk][2 + c]);
-            // P <= 2^kLazy and P v_top v_up <= kVPass
-            const float room = fminf(kLazy, kVPassLog2 - lg2_approx(v_top * v_up[nt][c]));
+            const float room = fminf(kLazy, kVPass - lg2_approx(v_top * v_up[nt][c]));
             pass = pass || fmaf(top[nt][c], f[nt][c], -m[nt][c]) > room;
           }
         if (__any_sync(0xffffffffu, pass)) {
-          float most[NT][2] = {};   // the row's largest P |s_V| in this step
-          float fo[NT][2];          // what O's sums are multiplied by
+          float most[NT][2];   // log2 of the row's largest P |s_V| in this step, P relative to a score of 0
+          float fo[NT][2];     // what O's sums are multiplied by
 #pragma unroll
           for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
             for (int c = 0; c < 2; ++c) {
-              const float best = quad_max(top[nt][c]), mx = f[nt][c] * best;
+              const float best = quad_max(top[nt][c]);
+              most[nt][c] = -INFINITY;
               fo[nt][c] = 1.f;
-              if (fmaf(best, f[nt][c], -m[nt][c]) > kLazy) {   // as above: no other row has a say in it
-                const float fm = ex2_approx(m[nt][c] - mx), up = fminf(v_up[nt][c] * ex2_approx(mx - m[nt][c]), kMostUp);
+              if (fmaf(best, f[nt][c], -m[nt][c]) > kLazy) {   // of this row alone
+                const float to = fmaf(best, f[nt][c], -kBelow), fm = ex2_approx(m[nt][c] - to);
+                const float up = fminf(v_up[nt][c] * ex2_approx(to - m[nt][c]), kMostUp);
                 fo[nt][c] = __fdividef(fm * up, v_up[nt][c]);   // 1, or less where v_up is at its end
                 v_up[nt][c] = up;
-                m[nt][c] = mx;
+                m[nt][c] = to;
                 l[nt][c] *= fm;
               }
             }
@@ -699,20 +714,25 @@ __global__ void __launch_bounds__(kThreads, (Shape<D, NT, C>::CtasPerSm)) fa_kv4
             uint32_t x = vs[0];
 #pragma unroll
             for (int e = 1; e < W / 2; ++e) x = max_abs2<BF16>(x, vs[e]);
-            const float sv = fmaxf(fabsf(kv4_scale<BF16>((uint16_t)x)), fabsf(kv4_scale<BF16>((uint16_t)(x >> 16))));
+            const float sv = lg2_approx(fmaxf(fabsf(kv4_scale<BF16>((uint16_t)x)), fabsf(kv4_scale<BF16>((uint16_t)(x >> 16)))));
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-              for (int c = 0; c < 2; ++c)
-                most[nt][c] = fmaxf(most[nt][c], ex2_approx(fmaf(sc[nt][i / 2][2 * (i % 2) + c], f[nt][c], -m[nt][c])) * sv);
+              for (int c = 0; c < 2; ++c) most[nt][c] = fmaxf(most[nt][c], fmaf(sc[nt][i / 2][2 * (i % 2) + c], f[nt][c], sv));
           }
 #pragma unroll
           for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
             for (int c = 0; c < 2; ++c) {
-              const float y = quad_max(most[nt][c]);
-              if (y * v_up[nt][c] > kVPass) {
-                const float up = pow2(6 + 127 - (int)(__float_as_uint(y) >> 23));   // y * up in [2^6, 2^7)
+              float z = quad_max(most[nt][c]) - m[nt][c];
+              if (z + lg2_approx(v_up[nt][c]) > kVPass) {
+                if (z > kMostV) {   // V near bf16's largest: m goes up instead
+                  m[nt][c] += kLazy;
+                  z -= kLazy;
+                  l[nt][c] *= 0x1p-56f;
+                  fo[nt][c] *= 0x1p-56f;
+                }
+                const float up = ex2_approx(6.f - z);
                 fo[nt][c] *= __fdividef(up, v_up[nt][c]);
                 v_up[nt][c] = up;
               }
@@ -853,7 +873,7 @@ __global__ void __launch_bounds__(kThreads, (Shape<D, NT, C>::CtasPerSm)) fa_kv4
           if (part != nullptr)
             *reinterpret_cast<float2*>(part + Sh::Rows * D + 2 * row) = make_float2(m[nt][c], ll);
           else
-            p.lse[row0 + row] = (m[nt][c] + log2f(ll)) * 0.69314718055994531f;
+            p.lse[row0 + row] = lse_of(m[nt][c], ll);
         }
       }
     if (!Near && begins && lane == 0 && (p.join_units || !ends)) {

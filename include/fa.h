@@ -325,7 +325,8 @@ int fa_fwd_fp8(const void* q, const void* k, const void* v, void* o, float* lse,
  *   the product with V's codes: by 2^-11 of itself down to 2^-20 of the row's
  *   largest P s, over the keys that the row sees, and by 2^-31 of that below.
  *   So a group of 32 of V's elements whose scales are less than 2^-20 of
- *   another group's loses bits (2^-22: 2^-9, ... 2^-31: all).  o, lse, scale as
+ *   another group's loses bits (2^-22: 2^-9, ... 2^-31: all).  A key whose weight
+ *   is below 2^-174 of the row's largest counts as having none.  o, lse, scale as
  *   in fa_fwd ([B,H,T,d], [B,H,T]; the *_O_F32 codes store O in float32, as
  *   fa_merge takes it).  Any T: what the cache holds is read once per 8 or 16
  *   rows of the T * H / Hkv that share a key head.  A prompt's first tokens,

@@ -385,3 +385,21 @@ def test_queries_of_any_magnitude_and_keys_that_make_up_for_it(e, H, d, wide):
     q = (torch.randn(1, H, 1, d, generator=c.g) * 2.0**e).bfloat16()
     attend(c, q, [299], o_fp32=True)
     _ok()
+
+
+@pytest.mark.parametrize("wide", [False, True])
+@pytest.mark.parametrize("H,d", [(1, 64), (4, 128), (8, 64), (12, 128)])
+def test_a_key_of_hardly_any_weight_and_the_largest_value_counts(H, d, wide):
+    """Weights of e^-88 to e^-102 times 3.4e38: below float32's smallest, and yet what O is made of; in the first step and
+    later, before and behind the key of the largest score, all that a warp has."""
+    for length, at, n in ((3, 0, 1), (3, 1, 1), (65, 64, 1), (300, 17, 1), (300, 250, 1), (300, 0, 64), (300, 64, 150), (1500, 700, 1)):
+        c = Cache(1, 1, d, "bf16", 16, length, seed=47)
+        k, v = _rows(c.g, "bf16", 1, 1, length, d) * 0.01, _rows(c.g, "bf16", 1, 1, length, d) * 2.0**-8
+        k[:, :, at : at + n], v[:, :, at : at + n] = -96 / d**0.5, float("inf")
+        c.write([0], length, k=k, v=v)
+        if wide:
+            _room(c)
+        for weak in (0.92, 0.96, 1.0, 1.06):
+            q = (weak * (1 + 0.01 * torch.rand(1, H, 1, d, generator=c.g))).bfloat16()
+            attend(c, q, [length - 1], o_fp32=True)
+    _ok()
