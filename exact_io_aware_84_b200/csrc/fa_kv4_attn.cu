@@ -52,16 +52,18 @@
 // to 2.9e-4 over 24 x 4 tokens of 128); two halves of P s_V would double the
 // products, of which a step has as many for V as for K.
 //
-// What bounds it.  Reading the cache once: 9D/8 bytes a key and key head.  At
-// d = 128 and up to 8 rows a warp issues about 240 instructions and 16 products
-// for 16 keys; with 12 warps a SM that is about 90 SM cycles where memory
-// needs 100, and the two overlap.  Measured on B200 (graph of calls): 8
-// sequences of 65536 keys and 8 rows 112 us, 5.4 TB/s; 64 sequences of up to
-// 8192 keys and 4 rows 68 us, 4.8 TB/s, about 14 us of both being the
-// start, the ends of units and the joining kernel; one sequence of 1000 keys
-// 8.0 us.  A product costs its pipe 8.5 cycles a SM quarter and delays the
-// integer instructions beside it (4 of them and 4 half-precision ones: 12.8),
-// so 24 products in place of 32 subtractions lost.
+// What bounds it.  Reading the cache once: 9D/8 bytes a key and key head, 104 SM
+// cycles for 16 keys at d = 128.  The steps of 64 sequences of up to 8192 keys
+// and 4 rows take 117, start and ends among them: 257 instructions and 16
+// products, which fill 56% of the issue slots and 45% of the integer pipe, the
+// busiest one.  No pipe is full, nor memory (58%): a warp's own chain of
+// dependent instructions, with three warps a scheduler, is what takes the time.
+// Measured on B200 (graph of calls): 8 sequences of 65536 keys and 8 rows 114 us,
+// 5.3 TB/s; 64 sequences of up to 8192 keys and 4 rows 69 us, 4.8 TB/s, about
+// 14 us of both being the start, the ends of units and the joining kernel; one
+// sequence of 1000 keys 8.5 us.  A product costs its pipe 8.5 cycles a SM
+// quarter and delays the integer instructions beside it (4 of them and 4
+// half-precision ones: 12.8), so 24 products in place of 32 subtractions lost.
 #include <cuda_runtime.h>
 
 #include <atomic>
@@ -964,11 +966,17 @@ __global__ void __launch_bounds__(kJoinThreads) fa_kv4_join_kernel(const Kv4FwdP
 }
 
 constexpr int kMaxSms = 160;
-// Most keys a warp for which a cluster a unit is the better division: 8 key
-// heads of one sequence, d = 128, four query heads each, take 13.4 us over 8192
-// keys (256 a warp) and 18.5 over 16384 (512), the other division 19.6 and
-// 22.4; 16 sequences of up to 9000 keys take 28.2 us in the other division and
-// would take 33.7 in clusters (600).
+// Most keys a warp for which a unit gets a cluster.  Clusters are faster where
+// units are many or short, the other division where a few long ones leave it
+// the whole GPU; no bound on this number alone is right for all (us in clusters,
+// in the other division; keys a warp):
+//   d = 128, 4 rows, 8 key heads: 1 sequence of 1000 (31) 8.4, 9.9; of 4096 (128)
+//     10.4, 11.2; of 8192 (256) 13.1, 12.4; of 16384 (512) 18.4, 16.0; 4 of 12000
+//     (375) 23.8, 21.0; 16 of up to 2000 14.4, 18.2; of 4096 (341) 22.5, 25.6; of
+//     5500 (458) 28.8, 32.3; of up to 9000 (750) 33.9, 28.7
+//   d = 64, 12 heads of one row: 8 of 1024 8.7, 11.3; of 6000 (300) 16.8, 18.5; of
+//     9500 (475) 22.4, 22.8
+//   d = 64, 384 rows a key head, 1 of 6000 (375) 24.0, 28.2; of 7800 (487) 28.4, 32.3
 constexpr int kNear = 512;
 
 // Lets a kernel have its dynamic shared memory, once per device.
@@ -997,8 +1005,10 @@ cudaError_t launch(Kv4FwdParams p, void* workspace, int sms, cudaStream_t st) {
   // Few and short units: a cluster each.  The largest cluster that has a step
   // for each warp and leaves an eighth of the GPU's places free (a cluster's
   // CTAs lie in one of its parts, so the last places do not fill: 144 units of
-  // 1000 keys, d = 64, take 10.0 us in clusters of 3 and 14.0 in clusters of 4),
-  // while no warp gets more than kNear keys.
+  // 1000 keys, d = 64, take 10.3 us in clusters of 3 and 14.4 in clusters of 4),
+  // while no warp gets more than kNear keys.  Lengths are on the device, so all
+  // this goes by the table's room for them: under a table for 131072 positions
+  // one sequence of 1000 keys takes 10.0 us instead of 8.4.
   const long long most = (((long long)p.c.max_pages << p.c.page_shift) + Sh::Step - 1) / Sh::Step;   // steps of a unit
   const long long places = (long long)sms * Sh::CtasPerSm * 7 / 8;
   int cluster = 8;
@@ -1013,9 +1023,10 @@ cudaError_t launch(Kv4FwdParams p, void* workspace, int sms, cudaStream_t st) {
   const int grid = (sms < kMaxSms ? sms : kMaxSms) * Sh::CtasPerSm;
   p.workers = grid * kWarps;
   // Few rows in all, and so many pieces to each: a row to a CTA of the joining
-  // kernel.  Else a CTA to each worker's last unit.  (64 units of 8 rows, 28
-  // pieces each: 115 us by row, 117 by worker; 96 units of 16 rows, 19 pieces:
-  // 44.5 and 40.5.)
+  // kernel.  Else a CTA to each worker's last unit.  us by row and by worker, of
+  // rows in all: d = 128, 64 rows 54.5, 75.5; 256 90, 97; 512 114, 117; 768 108,
+  // 108; 1024 109.8, 108.0; 1536 112.3, 108.0; 192 units of 16 rows 50.9, 41.7.  d = 64: 512 74.0, 76.0; 576 58.6, 59.5; 1024 72.8, 70.7; 1536 in units of
+  // one row 76.4, 77.3.
   p.join_units = units * Sh::Rows <= 4ll * sms;
   p.join_items = p.join_units ? D / 4 : 128;
   p.joins = static_cast<Kv4Join*>(workspace);
@@ -1031,12 +1042,18 @@ cudaError_t launch(Kv4FwdParams p, void* workspace, int sms, cudaStream_t st) {
 
 }  // namespace
 
-// Query rows that share a key head go in tiles of 8 columns.  One row in two
-// columns where four rows share a head: 64 sequences of up to 8192 keys, d =
-// 128, took 73.7 us against 77.7.  Two tiles a unit where more than 8 rows do: 64
-// sequences of 4096 keys and 12 rows, 106 us against 119 with one.  (Four,
-// where registers allow them at d = 64, lost: 18.4 against 14.8 us for two
-// sequences of 3000 keys and 384 rows a head.)
+// Query rows that share a key head go in tiles of 8 columns, two or four columns
+// to a row where few do.  64 sequences of up to 8192 keys, us with four, two and
+// one column a row: d = 128, 1 row 65.2, 66.7, 68.8; 2 rows 66.3, 68.3, 70.2; 4 rows
+// 68.7 with two and 70.1 with one; d = 64, 2 rows 46.4 and 47.0, 4 rows 47.3 and 47.7.
+// Two tiles a unit where more than 8 rows do.  24 sequences of up to 5000 keys,
+// us with two tiles and with one: d = 128, 9 rows 38.9, 40.3; 16 rows 41.1, 41.7;
+// d = 64, 9 rows 26.9, 27.3; 16 rows 28.3, 28.1; two sequences of 3000 keys and 384
+// rows, d = 64, 15.4, 18.2.  One tile is the better one where 17 to 24 rows do not
+// fill the second pair (24 rows: 60.9, 54.2; d = 64 39.8, 35.8) and for a short
+// sequence alone (1000 keys, 16 rows 11.4, 9.0).  (Four, where registers allow
+// them at d = 64, lost: 18.4 against 14.8 us for two sequences of 3000 keys and
+// 384 rows a head.)
 template <typename F>
 static auto kv4_variant(int d, long long rows, F&& f) {
   if (d == 128) {
