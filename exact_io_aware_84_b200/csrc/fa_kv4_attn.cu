@@ -39,7 +39,7 @@
 // moved (in log2); it moves only when a score passes that maximum by 8.  Weights
 // down to 2^-174 so stay in float32's range, for bf16 values reach 2^128.  v_up
 // follows the row's largest P |s_V| so far in the same way: it falls, bringing
-// that to 2^6 .. 2^7, when a bound on the step's passes 2^15, and it rises as m
+// that to 2^6, when a bound on the step's passes 2^15, and it rises as m
 // does, so that what O's sums are relative to does not change with m.  (Where
 // P |s_V| passes 2^120, m rises by 56 instead.)  A row thus rounds relative to
 // the products of the keys that it sees: keys of other rows, and keys of no
@@ -426,10 +426,11 @@ __global__ void __launch_bounds__(kThreads, (Shape<D, NT, C>::CtasPerSm)) fa_kv4
     long long rem = here - first_sum;   // steps behind the first one of sequence at.b
     at.b = first * per;
     Reach r = reach(at.b);
-    while (rem >= r.steps * p.units_per_seq) {
+    while (rem >= r.steps * p.units_per_seq && at.b < p.B - 1) {
       rem -= r.steps * p.units_per_seq;
       r = reach(++at.b);
     }
+    rem = min(rem, r.steps * p.units_per_seq - 1);   // nothing, unless lengths change under the call
     const unsigned u = (unsigned)((unsigned long long)rem / (unsigned)r.steps);
     at_step = (int)(rem - (long long)u * r.steps);
     at.h = (int)(u / (unsigned)p.row_tiles);
@@ -929,6 +930,11 @@ __global__ void __launch_bounds__(kJoinThreads) fa_kv4_join_kernel(const Kv4FwdP
   const Kv4Join j = p.joins[blockIdx.x];
   const int first = blockIdx.y * p.join_items;
   if (j.parts == 0 || j.rows * (D / 4) <= first) return;
+  // a record of this call is in range; lengths that change under the call, or a
+  // workspace that another one uses at the same time, can leave others
+  if (j.parts < 0 || j.parts >= p.workers || j.worker < 0 || j.worker >= p.workers - j.parts || j.rows > Sh::Rows || j.row < 0 ||
+      j.row > (long long)p.B * p.H * p.T - j.rows)
+    return;
   const int worker = j.worker;
   const int items = min(j.rows * (D / 4) - first, p.join_items), turns = min((int)blockDim.x / items, j.parts + 1);
   const int item = threadIdx.x % items, turn = threadIdx.x / items;

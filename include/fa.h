@@ -333,7 +333,7 @@ int fa_fwd_fp8(const void* q, const void* k, const void* v, void* o, float* lse,
  *   which see nothing before them, need no cache: fa_fwd_gqa suits them better.
  *   workspace: device buffer of fa_fwd_kv4_workspace_size bytes, 256-byte
  *   aligned, contents ignored on entry; calls that may overlap on the GPU need
- *   one each.
+ *   one each.  Neither start nor count may change while a call runs.
  *
  * Errors: FA_ERR_INVALID_ARG (NULL pointer other than count, non-positive
  * size, page size, H % Hkv, scale, max_pages * page or row count of 2^31 or
