@@ -58,10 +58,10 @@
 // products, which fill 56% of the issue slots and 45% of the integer pipe, the
 // busiest one.  No pipe is full, nor memory (58%): a warp's own chain of
 // dependent instructions, with three warps a scheduler, is what takes the time.
-// Measured on B200 (graph of calls): 8 sequences of 65536 keys and 8 rows 114 us,
+// Measured on B200 (graph of calls): 8 sequences of 65536 keys and 8 rows 115 us,
 // 5.3 TB/s; 64 sequences of up to 8192 keys and 4 rows 69 us, 4.8 TB/s, about
 // 14 us of both being the start, the ends of units and the joining kernel; one
-// sequence of 1000 keys 8.5 us.  A product costs its pipe 8.5 cycles a SM
+// sequence of 1000 keys 8.4 us.  A product costs its pipe 8.5 cycles a SM
 // quarter and delays the integer instructions beside it (4 of them and 4
 // half-precision ones: 12.8), so 24 products in place of 32 subtractions lost.
 #include <cuda_runtime.h>
